@@ -231,6 +231,114 @@ FAVOR_API favor_status favor_decode_step(const favor_shape *shape, const void *q
                                          const void *W, float *state, float *out, void *stream);
 
 /*
+ * Speculative decoding over the carried state. One round of a model whose layers use FAVOR+:
+ * favor_decode_tree answers a tree of drafted tokens in every layer without touching the state,
+ * favor_decode_verify walks the tree against the target's probabilities, and favor_decode_extend adds
+ * the accepted path (path and n_path as written by the walk, no copy to the host) to every layer's
+ * state. favor_decode_extend also forms the state of a prompt.
+ *
+ * A tree is B rows of T nodes in topological order: parents[b][i] is in -1 .. i-1, -1 for a root.
+ * Conditions on device data (a parent, count, token or index outside its range, probabilities without
+ * a finite positive sum) cannot be seen on the host: they are recorded as FAVOR_ERR_INVALID_ARG in the
+ * device status word (favor_sync_status), nothing is read or written out of range, and the entry point
+ * states what the result then is.
+ */
+/* Most nodes of a drafted tree. */
+#define FAVOR_TREE_MAX_NODES 128
+
+/*
+ * favor_decode_tree -- attention of a tree of drafted tokens over the carried state: node i sees every
+ * token of the state and J(i), its ancestors and itself,
+ *   out_i = [sum_r e^(w_r.q_i) (S_r + sum_{j in J(i)} e^(u_r(k_j)) v_j)]
+ *           / [sum_r e^(w_r.q_i) (z_r + sum_{j in J(i)} e^(u_r(k_j)))],
+ * the masked FA-part with J(i) in place of j <= i. A chain (parents[i] = i - 1) gives the rows of
+ * favor_decode_step fed the same tokens; a node without ancestors gives its first.
+ *
+ *   shape        : host pointer; L = T, the nodes per sequence, 1 .. FAVOR_TREE_MAX_NODES; dtype
+ *   q, k, v      : device, [B,H,T,d] in shape->dtype
+ *   W            : device, [m,d] in shape->dtype
+ *   state        : device, favor_decode_state_size bytes, read only (layout at favor_decode_step)
+ *   parents      : device, int32 [B,T] (an out-of-range parent is read as -1)
+ *   n_nodes      : device, int32 [B] nodes in use per sequence (0 .. T, clamped), or NULL for T each
+ *   out          : device, fp32 [B,H,T,d]; rows from n_nodes[b] on are left as they were
+ *   stream       : cudaStream_t as void*
+ * q, k, v, W, state, out 16-byte aligned, parents and n_nodes 4-byte. The result has fp32 precision for
+ * either dtype. What nodes outside J(i) hold never reaches row i, NaN and infinities included. Returns
+ * FAVOR_ERR_INVALID_ARG, FAVOR_ERR_UNSUPPORTED (T above the limit, d not 64/128, m not a multiple of
+ * 32 up to 256, B*H above 65535), FAVOR_ERR_CUDA.
+ */
+FAVOR_API favor_status favor_decode_tree(const favor_shape *shape, const void *q, const void *k, const void *v,
+                                         const void *W, const float *state, const int *parents, const int *n_nodes,
+                                         float *out, void *stream);
+
+/* favor_decode_extend_workspace_size -- device workspace bytes of favor_decode_extend for this shape
+ * and index width (0: no index); 0 if unsupported. */
+FAVOR_API size_t favor_decode_extend_workspace_size(const favor_shape *shape, int n_index);
+
+/*
+ * favor_decode_extend -- tokens added to the carried state: S_r += sum_j e^(u_r(k_j)) v_j,
+ * z_r += sum_j e^(u_r(k_j)), what favor_decode_step does to the state for one token after another.
+ * D_r becomes the largest u_r so far.
+ *
+ *   shape        : host pointer; L = tokens per sequence in k and v; dtype
+ *   k, v         : device, [B,H,L,d] in shape->dtype
+ *   W            : device, [m,d] in shape->dtype
+ *   index        : device, int32 [B,n_index]: the positions (0 .. L-1) of the tokens to add; one named
+ *                  twice is added twice, one out of range not at all. NULL (n_index = 0): 0, 1, ...
+ *   counts       : device, int32 [B]: how many of them, 0 .. n_index (0 .. L without index), clamped; a
+ *                  sequence with 0 keeps its state bit for bit. NULL: all. k, v and index behind the
+ *                  count are not read.
+ *   state        : device, favor_decode_state_size bytes, updated in place (all zeros: empty)
+ *   workspace    : device, >= favor_decode_extend_workspace_size bytes, 256-B aligned
+ *   stream       : cudaStream_t as void*
+ * k, v, W, state 16-byte aligned, index and counts 4-byte. fp32 precision for either dtype; the same
+ * inputs give the same bits. Errors as favor_decode_tree, and FAVOR_ERR_WORKSPACE.
+ */
+FAVOR_API favor_status favor_decode_extend(const favor_shape *shape, const void *k, const void *v, const void *W,
+                                           const int *index, int n_index, const int *counts, float *state,
+                                           void *workspace, size_t ws_bytes, void *stream);
+
+/* Problem shape of favor_decode_verify: B sequences, T nodes each, V vocabulary entries; dtype is the
+ * probabilities'. */
+typedef struct {
+    int B, T, V;
+    favor_dtype dtype;
+} favor_verify_shape;
+
+/*
+ * favor_decode_verify -- verification of a drafted tree against the target's probabilities with given
+ * random numbers, and the token that follows. Node 0 is the root: the last token already decided. The
+ * walk starts at cur = 0 with w = p[cur], Z = 1 and takes cur's children c in ascending order, with
+ * x = tokens[c]: accepted iff u[c] Z q[cur](x) < w(x), then cur = c, w = p[c], Z = 1; else the residual
+ * stays, w <- max(w - Z q[cur], 0), Z <- sum w. Where no child is left, next_token is the first y with
+ * sum_{y' <= y} w(y') > r sum w. With children drawn independently from q[cur] the emitted tokens are
+ * distributed as samples of the target.
+ *
+ *   shape        : host pointer; T in 1 .. FAVOR_TREE_MAX_NODES
+ *   parents      : device, int32 [B,T] (an out-of-range parent: the node is no one's child)
+ *   tokens       : device, int32 [B,T]; tokens[0] is not read as a draft (a drafted token outside 0 .. V-1
+ *                  is never accepted and takes nothing from w)
+ *   n_nodes      : device, int32 [B] nodes in use (0 .. T, clamped), or NULL for T each
+ *   p            : device, [B,T,V] in shape->dtype: row i the target's probabilities after node i. NaN and
+ *                  negative entries count as 0
+ *   q            : device, [B,T,V]: row i the probabilities node i's children were drawn from; or NULL for a
+ *                  deterministic draft (point masses: q(x) = 1; rejected, Z <- Z - w(x) and w(x) <- 0)
+ *   u            : device, fp32 [B,T]: node c's acceptance number, in [0, 1)
+ *   r            : device, fp32 [B]: the sample's number, in [0, 1)
+ *   path         : device, int32 [B,T]: the accepted nodes from node 0 on, then -1
+ *   n_path       : device, int32 [B]: how many (0 only where n_nodes is 0)
+ *   next_token   : device, int32 [B]: the sampled token. Where w is 0 everywhere it is sampled from p[cur];
+ *                  where that has no finite positive sum either, or n_nodes is 0, it is -1
+ *   stream       : cudaStream_t as void*
+ * p and q 16-byte aligned, the others 4-byte. Sums and residuals are fp64; no result depends on the order
+ * blocks run in. Returns FAVOR_ERR_INVALID_ARG, FAVOR_ERR_UNSUPPORTED (T above the limit, B above 65535),
+ * FAVOR_ERR_CUDA.
+ */
+FAVOR_API favor_status favor_decode_verify(const favor_verify_shape *shape, const int *parents, const int *tokens,
+                                           const int *n_nodes, const void *p, const void *q, const float *u,
+                                           const float *r, int *path, int *n_path, int *next_token, void *stream);
+
+/*
  * Sequence-parallel bidirectional forward (bf16). The keys of one sequence may be spread over
  * several calls -- one per rank, each holding a contiguous run of every head's tokens: the FA-part
  * needs only the sums (K')^T V and (K')^T 1_L over all keys ("Fast Attention Via Positive

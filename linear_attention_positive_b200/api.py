@@ -37,6 +37,10 @@ EXPORTS = (
     "favor_sp_output",
     "favor_decode_state_size",
     "favor_decode_step",
+    "favor_decode_tree",
+    "favor_decode_extend_workspace_size",
+    "favor_decode_extend",
+    "favor_decode_verify",
     "favor_selftest_bounded_wait",
     "favor_fwd_static_scratch",
 )
@@ -54,7 +58,12 @@ class Shape(ctypes.Structure):
                 ("m", ctypes.c_int), ("dtype", ctypes.c_int)]
 
 
+class VerifyShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("V", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
 FAVOR_MAX_STAGES = 24
+FAVOR_TREE_MAX_NODES = 128
 
 
 FAVOR_MAP_POSITIVE = 0
@@ -106,6 +115,14 @@ def library():
     lib.favor_decode_state_size.restype = Z
     lib.favor_decode_step.argtypes = [SP, P, P, P, P, P, P, P]
     lib.favor_decode_step.restype = I
+    lib.favor_decode_tree.argtypes = [SP, P, P, P, P, P, P, P, P, P]
+    lib.favor_decode_tree.restype = I
+    lib.favor_decode_extend_workspace_size.argtypes = [SP, I]
+    lib.favor_decode_extend_workspace_size.restype = Z
+    lib.favor_decode_extend.argtypes = [SP, P, P, P, P, I, P, P, P, Z, P]
+    lib.favor_decode_extend.restype = I
+    lib.favor_decode_verify.argtypes = [ctypes.POINTER(VerifyShape), P, P, P, P, P, P, P, P, P, P, P]
+    lib.favor_decode_verify.restype = I
     lib.favor_selftest_bounded_wait.argtypes = [ctypes.c_uint, P]
     lib.favor_selftest_bounded_wait.restype = I
     lib.favor_fwd_static_scratch.argtypes = [SP, P, P, P, P, P, P]
@@ -329,6 +346,109 @@ def decode_step(q, k, v, W, state, out=None, stream=None):
                                      _ptr(out), _stream_ptr(stream))
     _check(st, "favor_decode_step")
     return out
+
+
+def _check_like(name, t, shape, dtype, device):
+    """An argument beside the main tensors: contiguous, of this shape, type and device (None passes)."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise FavorError(FAVOR_ERR_INVALID_ARG,
+                         f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
+def _check_tokens(first, rest, W, state):
+    """Token tensors [B,H,L,d] of one shape, W [m,d] and a carried state, on one CUDA device."""
+    _check_inputs((first, *rest, W), first)
+    if first.dim() != 4 or W.dim() != 2 or W.shape[1] != first.shape[3]:
+        raise FavorError(FAVOR_ERR_INVALID_ARG, "tokens must be [B,H,L,d] and W [m,d]")
+    for t in (*rest, W):
+        if t.device != first.device:
+            raise FavorError(FAVOR_ERR_INVALID_ARG, "tensors must be on one device")
+        if t is not W and t.shape != first.shape:
+            raise FavorError(FAVOR_ERR_INVALID_ARG, "token tensors must have one shape")
+    torch = _torch()
+    B, H, _, d = first.shape
+    m = W.shape[0]
+    if not state.is_contiguous() or state.dtype != torch.float32 or state.device != first.device or \
+            state.numel() != B * H * (d + 2) * m:
+        raise FavorError(FAVOR_ERR_INVALID_ARG, "state must come from decode_state() for these B, H, d, m and device")
+
+
+def decode_tree(q, k, v, W, state, parents, n_nodes=None, out=None, stream=None):
+    """Attention of a tree of drafted tokens over the carried state, through favor_decode_tree. q, k, v:
+    [B,H,T,d] (bf16 or fp32), T up to FAVOR_TREE_MAX_NODES nodes in topological order; state from
+    decode_state(), read only; parents: int32 [B,T], -1 for a root; n_nodes: int32 [B] or None. Returns
+    the fp32 output [B,H,T,d]; its rows from n_nodes[b] on are left as they were in ``out`` (undefined
+    when ``out`` is None)."""
+    torch = _torch()
+    _check_tokens(q, (k, v), W, state)
+    B, H, T, d = q.shape
+    _check_like("parents", parents, (B, T), torch.int32, q.device)
+    _check_like("n_nodes", n_nodes, (B,), torch.int32, q.device)
+    _check_like("out", out, q.shape, torch.float32, q.device)
+    shape = _shape_of(q, W)
+    with torch.cuda.device(q.device):
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+        st = library().favor_decode_tree(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(W), _ptr(state),
+                                         _ptr(parents), _ptr(n_nodes), _ptr(out), _stream_ptr(stream))
+    _check(st, "favor_decode_tree")
+    return out
+
+
+def decode_extend(k, v, W, state, index=None, counts=None, workspace=None, stream=None):
+    """Tokens added to the carried state, through favor_decode_extend. k, v: [B,H,L,d] (bf16 or fp32);
+    state from decode_state(), updated in place and returned; index: int32 [B,N] positions of the tokens
+    to add (such as the path decode_verify returns) or None for all in order; counts: int32 [B] how many
+    of them, or None."""
+    torch = _torch()
+    _check_tokens(k, (v,), W, state)
+    B = k.shape[0]
+    if index is not None and (index.dim() != 2 or index.shape[1] == 0):
+        raise FavorError(FAVOR_ERR_INVALID_ARG, "index must be [B,N], N >= 1")
+    n_index = 0 if index is None else index.shape[1]
+    _check_like("index", index, (B, n_index), torch.int32, k.device)
+    _check_like("counts", counts, (B,), torch.int32, k.device)
+    shape = _shape_of(k, W)
+    lib = library()
+    with torch.cuda.device(k.device):
+        if workspace is None:
+            ws_n = lib.favor_decode_extend_workspace_size(ctypes.byref(shape), n_index)
+            if ws_n == 0:
+                raise FavorError(FAVOR_ERR_UNSUPPORTED, "favor_decode_extend_workspace_size")
+            workspace = _alloc_bytes(ws_n, k.device)
+        st = lib.favor_decode_extend(ctypes.byref(shape), _ptr(k), _ptr(v), _ptr(W), _ptr(index), n_index,
+                                     _ptr(counts), _ptr(state), _ptr(workspace), workspace.numel(),
+                                     _stream_ptr(stream))
+    _check(st, "favor_decode_extend")
+    return state
+
+
+def decode_verify(parents, tokens, p, u, r, q=None, n_nodes=None, stream=None):
+    """Verification of a drafted tree through favor_decode_verify. parents, tokens: int32 [B,T]; p, q:
+    [B,T,V] bf16 or fp32 probabilities of the target and the draft (q None: a deterministic draft); u:
+    fp32 [B,T], r: fp32 [B] uniform numbers in [0, 1). Returns (path [B,T], n_path [B], next_token [B]),
+    int32: path and n_path go to decode_extend as index and counts."""
+    torch = _torch()
+    _check_inputs((p,) if q is None else (p, q), p)
+    if p.dim() != 3:
+        raise FavorError(FAVOR_ERR_INVALID_ARG, "p must be [B,T,V]")
+    B, T, V = p.shape
+    _check_like("q", q, p.shape, p.dtype, p.device)
+    _check_like("parents", parents, (B, T), torch.int32, p.device)
+    _check_like("tokens", tokens, (B, T), torch.int32, p.device)
+    _check_like("n_nodes", n_nodes, (B,), torch.int32, p.device)
+    _check_like("u", u, (B, T), torch.float32, p.device)
+    _check_like("r", r, (B,), torch.float32, p.device)
+    shape = VerifyShape(B, T, V, _dtype_code(p))
+    with torch.cuda.device(p.device):
+        path, n_path, token = (torch.empty(s, dtype=torch.int32, device=p.device) for s in ((B, T), (B,), (B,)))
+        st = library().favor_decode_verify(ctypes.byref(shape), _ptr(parents), _ptr(tokens), _ptr(n_nodes), _ptr(p),
+                                           _ptr(q), _ptr(u), _ptr(r), _ptr(path), _ptr(n_path), _ptr(token),
+                                           _stream_ptr(stream))
+    _check(st, "favor_decode_verify")
+    return path, n_path, token
 
 
 def selftest_bounded_wait(limit_us, stream=None):

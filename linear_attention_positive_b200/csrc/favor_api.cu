@@ -21,6 +21,9 @@
 #include "k_gemm.cu"
 #include "k_selftest.cu"
 #include "k_decode.cu"
+#include "k_decode_tree.cu"
+#include "k_decode_extend.cu"
+#include "k_decode_verify.cu"
 
 namespace favor {
 namespace {
@@ -1088,6 +1091,92 @@ extern "C" favor_status favor_decode_step(const favor_shape *s, const void *q, c
         return FAVOR_ERR_UNSUPPORTED;
     DecodeParams p{s->B * s->H, s->m, s->dtype == FAVOR_BF16 ? 1 : 0, q, k, v, W, state, out};
     return cuda_status(launch_decode_step(p, s->d, (cudaStream_t)stream));
+}
+
+// ----------------------------------------------- drafted trees over the carried decoding state
+
+namespace favor {
+namespace {
+
+bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+
+// What the decoding calls implement (as favor_decode_step).
+bool decode_supported(const favor_shape *s) {
+    return (s->d == 64 || s->d == 128) && s->m % 32 == 0 && s->m <= 256 && (long long)s->B * s->H <= 65535;
+}
+
+// Runs of tokens per head of favor_decode_extend, and tokens per run. Up to kExtWhole tokens (an
+// accepted path, a short prompt) the state is updated in place by one CTA a head; longer inputs are
+// cut so that about four CTAs an SM are in flight.
+constexpr int kExtWhole = 32;
+struct ExtendPlan {
+    int n_split, tok_per_split;
+};
+ExtendPlan extend_plan(const favor_shape *s, int n_tok) {
+    if (n_tok <= kExtWhole) return {1, n_tok};
+    const long long BH = (long long)s->B * s->H, ctas = 4ll * num_sms();
+    long long per = std::max<long long>(kExtWhole, (BH * n_tok + ctas - 1) / ctas);
+    per = std::min<long long>((per + kExtTok - 1) / kExtTok * kExtTok, n_tok);
+    return {(int)((n_tok + per - 1) / per), (int)per};
+}
+
+}  // namespace
+}  // namespace favor
+
+extern "C" favor_status favor_decode_tree(const favor_shape *s, const void *q, const void *k, const void *v,
+                                          const void *W, const float *state, const int *parents, const int *n_nodes,
+                                          float *out, void *stream) {
+    if (!shape_ok(s) || q == nullptr || k == nullptr || v == nullptr || W == nullptr || state == nullptr ||
+        parents == nullptr || out == nullptr)
+        return FAVOR_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(W) || !aligned16(state) || !aligned16(out) ||
+        !aligned4(parents) || !aligned4(n_nodes))
+        return FAVOR_ERR_INVALID_ARG;
+    if (!decode_supported(s) || s->L > FAVOR_TREE_MAX_NODES) return FAVOR_ERR_UNSUPPORTED;
+    TreeParams p{s->B, s->H, s->L, s->m, s->dtype == FAVOR_BF16 ? 1 : 0, q, k, v, W, state, parents, n_nodes, out};
+    return cuda_status(launch_decode_tree(p, s->d, (cudaStream_t)stream));
+}
+
+extern "C" size_t favor_decode_extend_workspace_size(const favor_shape *s, int n_index) {
+    if (!shape_ok(s) || n_index < 0 || !decode_supported(s)) return 0;
+    const ExtendPlan pl = extend_plan(s, n_index > 0 ? n_index : s->L);
+    if (pl.n_split == 1) return 256;
+    return align256((size_t)s->B * s->H * pl.n_split * ((size_t)s->d * s->m + 2 * s->m) * 4);
+}
+
+extern "C" favor_status favor_decode_extend(const favor_shape *s, const void *k, const void *v, const void *W,
+                                            const int *index, int n_index, const int *counts, float *state,
+                                            void *workspace, size_t ws_bytes, void *stream) {
+    if (!shape_ok(s) || k == nullptr || v == nullptr || W == nullptr || state == nullptr)
+        return FAVOR_ERR_INVALID_ARG;
+    if ((index == nullptr) != (n_index == 0) || n_index < 0) return FAVOR_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(W) || !aligned16(state) || !aligned4(index) || !aligned4(counts))
+        return FAVOR_ERR_INVALID_ARG;
+    if (!decode_supported(s)) return FAVOR_ERR_UNSUPPORTED;
+    if (workspace == nullptr || ((uintptr_t)workspace & 255u) != 0 ||
+        ws_bytes < favor_decode_extend_workspace_size(s, n_index))
+        return FAVOR_ERR_WORKSPACE;
+    const int n_tok = n_index > 0 ? n_index : s->L;
+    const ExtendPlan pl = extend_plan(s, n_tok);
+    ExtendParams p{s->B, s->H, s->L, s->m, s->dtype == FAVOR_BF16 ? 1 : 0, k, v, W, index, counts, n_tok, state,
+                   (float *)workspace, pl.n_split, pl.tok_per_split};
+    return cuda_status(launch_decode_extend(p, s->d, (cudaStream_t)stream));
+}
+
+extern "C" favor_status favor_decode_verify(const favor_verify_shape *s, const int *parents, const int *tokens,
+                                            const int *n_nodes, const void *p, const void *q, const float *u,
+                                            const float *r, int *path, int *n_path, int *next_token, void *stream) {
+    if (s == nullptr || s->B <= 0 || s->T <= 0 || s->V <= 0 || (s->dtype != FAVOR_F32 && s->dtype != FAVOR_BF16))
+        return FAVOR_ERR_INVALID_ARG;
+    if (parents == nullptr || tokens == nullptr || p == nullptr || u == nullptr || r == nullptr || path == nullptr ||
+        n_path == nullptr || next_token == nullptr)
+        return FAVOR_ERR_INVALID_ARG;
+    if (!aligned16(p) || !aligned16(q) || !aligned4(parents) || !aligned4(tokens) || !aligned4(n_nodes) ||
+        !aligned4(u) || !aligned4(r) || !aligned4(path) || !aligned4(n_path) || !aligned4(next_token))
+        return FAVOR_ERR_INVALID_ARG;
+    if (s->T > FAVOR_TREE_MAX_NODES || s->B > 65535) return FAVOR_ERR_UNSUPPORTED;
+    VerifyParams a{s->B, s->T, s->V, parents, tokens, n_nodes, p, q, u, r, path, n_path, next_token};
+    return cuda_status(launch_decode_verify(a, s->dtype == FAVOR_BF16, (cudaStream_t)stream));
 }
 
 // ------------------------------------------------------------------ sequence-parallel forward

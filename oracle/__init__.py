@@ -28,10 +28,11 @@ Modules
 ``favor``    phi, bidirectional / causal forward, backward, the single-token causal step,
              brute-force definitions, softmax.
 ``kernels``  generalised attention (ReLU features) and the trigonometric softmax features.
+``speculative`` drafted trees over the carried state: attention, verification walk, extension.
 
 Every function here is pinned by ``tests/test_oracle_*.py`` against something other than itself
 (a library routine, brute force on the explicit L x L matrix, closed forms, Monte-Carlo bounds,
 invariants, finite differences). No function is "parity unpinned".
 """
 
-from . import philox, features, favor, kernels  # noqa: F401
+from . import philox, features, favor, kernels, speculative  # noqa: F401

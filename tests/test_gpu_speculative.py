@@ -1,0 +1,578 @@
+"""GPU parity of the drafted-tree calls (favor_decode_tree, favor_decode_extend, favor_decode_verify)
+with the fp64 oracle.
+
+Tolerance: the calls compute with fp32 precision for either input type, so the fp32 bound
+1e-4 * RMS of favor_decode_step's tests applies to outputs. Where it comes from: the exponent u of a
+feature is a sum of d products in fp32 and its absolute error is its features' relative error. With
+|w| <= 16 and |x| <= 5 the d <= 128 products sum in magnitude to at most |w| |x| <= 80; each partial
+sum is rounded by at most 80 2^-24, in all 128 * 80 * 6e-8 = 6e-4 at worst, and 1/sqrt(128) of that
+(5e-5) with the roundings' signs mixed; outputs average features, which lowers it further. State
+entries are compared per entry relative to the largest of their kind, with the same 1e-4."""
+
+import numpy as np
+import pytest
+import torch
+
+from linear_attention_positive_b200 import api
+from oracle import speculative
+from tests.helpers import features_for, rel_max_err, to_torch
+
+pytestmark = pytest.mark.gpu
+
+TOL = 1e-4
+
+
+class Problem:
+    """Seeded tokens, features and a carried state (after ``prior`` tokens) on both sides."""
+
+    def __init__(self, B, H, T, d, m, dtype, device, prior=40, seed=0):
+        g = np.random.default_rng(seed)
+        self.B, self.H, self.T, self.d, self.m, self.dtype, self.device = B, H, T, d, m, dtype, device
+        self.g = g
+        self.Wr, self.W64 = features_for(3, m, d, dtype)
+        self.W = to_torch(self.Wr, dtype, device)
+        self.q, self.k, self.v = (self.tokens(T, d ** -0.25 if i < 2 else 1.0) for i in range(3))
+        self.prior = [self.tokens(prior, d ** -0.25 if i < 2 else 1.0) for i in range(3)] if prior else None
+        self.state = api.decode_state(B, H, d, m, device)
+        for t in range(prior):
+            api.decode_step(*(x[:, :, t].contiguous() for x in self.prior), self.W, self.state)
+
+    def tokens(self, n, scale):
+        return to_torch(self.g.standard_normal((self.B, self.H, n, self.d)) * scale, self.dtype, self.device)
+
+    def head(self, x, b, h):
+        return x[b, h].double().cpu().numpy()
+
+    def oracle_state(self, b, h):
+        S, z = np.zeros((self.m, self.d)), np.zeros(self.m)
+        if self.prior is None:
+            return S, z
+        return speculative.decode_extend(S, z, self.head(self.prior[1], b, h), self.head(self.prior[2], b, h), self.W64)
+
+    def gpu_state(self, state=None):
+        """True sums S [B,H,m,d], z [B,H,m] of a device state, in the oracle's scale."""
+        t = (self.state if state is None else state).double().cpu().numpy().reshape(self.B, self.H, self.d + 2, self.m)
+        scale = np.where(t[:, :, self.d] != 0, np.exp(t[:, :, self.d + 1]), 0.0) / np.sqrt(self.m)
+        return np.swapaxes(t[:, :, : self.d] * scale[:, :, None], 2, 3), t[:, :, self.d] * scale
+
+    def oracle_tree(self, parents, n_nodes=None):
+        out = np.full((self.B, self.H, self.T, self.d), np.nan)
+        for b in range(self.B):
+            n = self.T if n_nodes is None else n_nodes[b]
+            for h in range(self.H):
+                S, z = self.oracle_state(b, h)
+                X = [self.head(x, b, h)[:n] for x in (self.q, self.k, self.v)]
+                out[b, h, :n] = speculative.decode_tree(S, z, *X, self.W64, list(parents[b][:n]))
+        return out
+
+
+def i32(x, device):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device=device)
+
+
+def random_parents(B, T, seed=0, reach=12):
+    g = np.random.default_rng(seed)
+    return np.array([[-1 if i == 0 else int(g.integers(max(0, i - reach), i)) for i in range(T)] for _ in range(B)])
+
+
+def status_ok():
+    assert api.sync_status() == api.FAVOR_OK
+
+
+# --------------------------------------------------------------------------------------------- tree
+
+SHAPES = [(1, 1, 1, 64, 32), (2, 3, 1, 128, 256), (2, 2, 2, 64, 96), (1, 2, 4, 64, 256), (2, 2, 5, 128, 160),
+          (2, 2, 16, 64, 128), (1, 3, 17, 64, 256), (2, 2, 33, 128, 96), (2, 2, 64, 64, 256), (1, 2, 65, 64, 224),
+          (1, 2, 127, 128, 128), (1, 1, 128, 128, 256), (1, 2, 128, 64, 256), (3, 5, 40, 64, 64)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("prior", [40, 0])
+@pytest.mark.parametrize("B,H,T,d,m", SHAPES)
+def test_tree_matches_oracle(cuda_device, dtype, prior, B, H, T, d, m):
+    x = Problem(B, H, T, d, m, dtype, cuda_device, prior=prior, seed=T)
+    parents = random_parents(B, T, seed=T)
+    before = x.state.clone()
+    out = api.decode_tree(x.q, x.k, x.v, x.W, x.state, i32(parents, cuda_device))
+    status_ok()
+    assert rel_max_err(out.double().cpu().numpy(), x.oracle_tree(parents)) <= TOL
+    assert torch.equal(before, x.state)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["chain", "star", "forest"])
+@pytest.mark.parametrize("T", [3, 48, 128])
+def test_tree_shapes_at_the_extremes(cuda_device, dtype, kind, T):
+    """A chain (every row sees all before it), a star (two nodes a row) and a forest of lone roots."""
+    x = Problem(2, 2, T, 64, 256, dtype, cuda_device, seed=5)
+    one = {"chain": np.arange(T) - 1, "star": np.where(np.arange(T) > 0, 0, -1), "forest": np.full(T, -1)}[kind]
+    parents = np.stack([one] * 2)
+    out = api.decode_tree(x.q, x.k, x.v, x.W, x.state, i32(parents, cuda_device))
+    status_ok()
+    assert rel_max_err(out.double().cpu().numpy(), x.oracle_tree(parents)) <= TOL
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_tree_chain_is_repeated_steps(cuda_device, dtype):
+    x = Problem(2, 3, 24, 64, 256, dtype, cuda_device, seed=9)
+    parents = np.stack([np.arange(24) - 1] * 2)
+    out = api.decode_tree(x.q, x.k, x.v, x.W, x.state, i32(parents, cuda_device))
+    steps = [api.decode_step(*(y[:, :, t].contiguous() for y in (x.q, x.k, x.v)), x.W, x.state) for t in range(24)]
+    status_ok()
+    assert rel_max_err(out.double().cpu().numpy(), torch.stack(steps, 2).double().cpu().numpy()) <= TOL
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,T", [(64, 70), (128, 24)])
+def test_tree_padding_is_neither_read_nor_written(cuda_device, dtype, d, T):
+    x = Problem(4, 2, T, d, 128, dtype, cuda_device, seed=3)
+    counts = [T, 0, 1, T // 2 + 1]
+    parents = random_parents(4, T, seed=3)
+    for b, n in enumerate(counts):
+        for y in (x.q, x.k, x.v):
+            y[b, :, n:] = float("nan")
+        parents[b, n:] = 10**6
+    out = torch.full((4, 2, T, d), 7.0, device=cuda_device)
+    api.decode_tree(x.q, x.k, x.v, x.W, x.state, i32(parents, cuda_device), n_nodes=i32(counts, cuda_device), out=out)
+    status_ok()
+    ref = x.oracle_tree(parents, counts)
+    got = out.double().cpu().numpy()
+    for b, n in enumerate(counts):
+        assert (got[b, :, n:] == 7.0).all()
+        if n:
+            assert rel_max_err(got[b, :, :n], ref[b, :, :n]) <= TOL
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("where", ["k", "v", "q"])
+def test_tree_unseen_nodes_do_not_reach_a_row(cuda_device, dtype, bad, where):
+    """Node 5 holds NaN or infinities; only the rows below it may show them."""
+    T = 40
+    x = Problem(1, 2, T, 64, 256, dtype, cuda_device, seed=4)
+    parents = random_parents(1, T, seed=4)
+    ref = x.oracle_tree(parents)
+    getattr(x, where)[:, :, 5] = bad
+    out = api.decode_tree(x.q, x.k, x.v, x.W, x.state, i32(parents, cuda_device))
+    status_ok()
+    got = out.double().cpu().numpy()
+    sees = [5 in speculative.ancestors(list(parents[0]), i) if where != "q" else i == 5 for i in range(T)]
+    clean = [i for i in range(T) if not sees[i]]
+    assert rel_max_err(got[:, :, clean], ref[:, :, clean]) <= TOL
+    if where == "v":  # what a row does see, it shows
+        dirty = [i for i in range(T) if sees[i]]
+        assert not np.isfinite(got[:, :, dirty]).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [4.0, 8.0])
+@pytest.mark.parametrize("prior", [40, 0])
+def test_tree_unseen_nodes_with_far_larger_logits(cuda_device, dtype, scale, prior):
+    """Keys of very different norms and directions in one tree: features that unseen nodes dominate by
+    hundreds of nats leave a row its own terms. The exponents reach |w| |x| ~ 16 * 40, so the
+    tolerance grows with them: u's rounding error is 640 / 80 of the bound above."""
+    T = 48
+    x = Problem(1, 2, T, 64, 128, dtype, cuda_device, prior=prior, seed=6)
+    parents = random_parents(1, T, seed=6, reach=30)
+    x.k[:, :, 3::4] *= scale
+    x.q[:, :, 1::3] *= -scale
+    out = api.decode_tree(x.q, x.k, x.v, x.W, x.state, i32(parents, cuda_device))
+    status_ok()
+    got, ref = out.double().cpu().numpy(), x.oracle_tree(parents)
+    assert np.isfinite(got).all()
+    assert rel_max_err(got, ref) <= 8 * TOL
+
+
+def test_tree_bad_parents_and_counts_are_recorded(cuda_device):
+    T = 20
+    x = Problem(2, 2, T, 64, 128, "bf16", cuda_device, seed=8)
+    parents = random_parents(2, T, seed=8)
+    read = parents.copy()
+    for i, p in ((3, 3), (7, 12), (9, -5), (11, 2**30)):
+        parents[1, i], read[1, i] = p, -1
+    out = api.decode_tree(x.q, x.k, x.v, x.W, x.state, i32(parents, cuda_device), n_nodes=i32([T, T], cuda_device))
+    assert api.sync_status() == api.FAVOR_ERR_INVALID_ARG
+    assert rel_max_err(out.double().cpu().numpy(), x.oracle_tree(read)) <= TOL
+    out = api.decode_tree(x.q, x.k, x.v, x.W, x.state, i32(read, cuda_device), n_nodes=i32([T + 5, -1], cuda_device),
+                          out=torch.zeros_like(out))
+    assert api.sync_status() == api.FAVOR_ERR_INVALID_ARG
+    assert rel_max_err(out[0].double().cpu().numpy(), x.oracle_tree(read)[0]) <= TOL and (out[1] == 0).all()
+    status_ok()
+
+
+# ------------------------------------------------------------------------------------------- extend
+
+def check_state(x, state, chosen):
+    """A device state against the oracle's after adding the chosen token positions of each sequence."""
+    S, z = x.gpu_state(state)
+    for b in range(x.B):
+        for h in range(x.H):
+            S0, z0 = x.oracle_state(b, h)
+            Sr, zr = speculative.decode_extend(S0, z0, x.head(x.k, b, h), x.head(x.v, b, h), x.W64, chosen[b])
+            assert np.abs(S[b, h] - Sr).max() <= TOL * np.abs(Sr).max()
+            assert np.abs(z[b, h] - zr).max() <= TOL * np.abs(zr).max()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("prior", [40, 0])
+@pytest.mark.parametrize("B,H,L,d,m", [(1, 1, 1, 64, 32), (2, 3, 7, 128, 256), (2, 2, 32, 64, 96), (2, 2, 33, 64, 256),
+                                       (1, 3, 129, 128, 160), (2, 2, 500, 64, 128), (1, 2, 1500, 128, 256),
+                                       (1, 2, 3001, 64, 256), (3, 1, 900, 64, 224)])
+def test_extend_matches_oracle(cuda_device, dtype, prior, B, H, L, d, m):
+    x = Problem(B, H, L, d, m, dtype, cuda_device, prior=prior, seed=L)
+    old = x.state.clone()
+    state = api.decode_extend(x.k, x.v, x.W, x.state)
+    status_ok()
+    assert state is x.state
+    check_state(x, state, [None] * B)
+    # D is the largest logit so far
+    t = state.view(B, H, d + 2, m)[:, :, d + 1].double().cpu().numpy()
+    for b in range(B):
+        for h in range(H):
+            k = np.concatenate([x.head(x.k, b, h)] + ([x.head(x.prior[1], b, h)] if prior else []))
+            u = (k @ x.W64.T - 0.5 * (k * k).sum(1, keepdims=True)).max(0)
+            assert np.abs(t[b, h] - u).max() <= TOL
+    # the same bits again
+    again = api.decode_extend(x.k, x.v, x.W, old)
+    assert torch.equal(again, state)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("L,d,m", [(64, 64, 256), (64, 128, 96), (2000, 64, 256), (700, 128, 128)])
+def test_extend_counts_and_padding(cuda_device, dtype, L, d, m):
+    x = Problem(4, 2, L, d, m, dtype, cuda_device, seed=L + 1)
+    counts = [L, 0, 1, L // 3]
+    for b, n in enumerate(counts):
+        x.k[b, :, n:] = float("nan")
+        x.v[b, :, n:] = float("inf")
+    old = x.state.clone()
+    state = api.decode_extend(x.k, x.v, x.W, x.state, counts=i32(counts, cuda_device))
+    status_ok()
+    check_state(x, state, [list(range(n)) for n in counts])
+    assert torch.equal(state.view(4, -1)[1], old.view(4, -1)[1])  # bit for bit
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [1, 9, 60])
+def test_extend_by_index(cuda_device, dtype, N):
+    """An accepted path, the same position twice, and positions in any order."""
+    L = 64
+    x = Problem(3, 2, L, 64, 256, dtype, cuda_device, seed=N)
+    index = x.g.integers(0, L, (3, N))
+    counts = [N, max(N - 2, 1), 0]
+    state = api.decode_extend(x.k, x.v, x.W, x.state, index=i32(index, cuda_device), counts=i32(counts, cuda_device))
+    status_ok()
+    check_state(x, state, [index[b, :n].tolist() for b, n in enumerate(counts)])
+
+
+def test_extend_bad_index_and_counts_are_recorded(cuda_device):
+    L = 40
+    x = Problem(2, 2, L, 64, 128, "bf16", cuda_device, seed=2)
+    index = np.array([[3, L, 5, -1, 7], [L + 9, -3, 2**30, L, -1]])
+    old = x.state.clone()
+    state = api.decode_extend(x.k, x.v, x.W, x.state, index=i32(index, cuda_device))
+    assert api.sync_status() == api.FAVOR_ERR_INVALID_ARG
+    check_state(x, state, [[3, 5, 7], []])
+    state = api.decode_extend(x.k, x.v, x.W, old, counts=i32([L + 1, -7], cuda_device))
+    assert api.sync_status() == api.FAVOR_ERR_INVALID_ARG
+    check_state(x, state, [list(range(L)), []])
+    status_ok()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("L", [20, 700])
+def test_extend_keys_far_above_and_below_earlier_ones(cuda_device, dtype, L):
+    """Keys whose logits jump by tens of nats over earlier ones (rescaling what was summed), and keys far
+    below them (nothing may turn into NaN)."""
+    x = Problem(1, 2, L, 64, 128, dtype, cuda_device, seed=1)
+    x.k[:, :, L // 2] = (0.9 * x.W[0].float()).to(x.k.dtype)
+    x.k[:, :, L - 3:] *= 12
+    state = api.decode_extend(x.k, x.v, x.W, x.state)
+    status_ok()
+    t = state.view(2, 66, 128).double().cpu().numpy()
+    assert np.isfinite(t).all()
+    # per feature, relative to that feature's own sums: u reaches |w| |x| ~ 16 * 34, 7 times the bound above
+    for h in range(2):
+        S0, z0 = x.oracle_state(0, h)
+        Sr, zr = speculative.decode_extend(S0, z0, x.head(x.k, 0, h), x.head(x.v, 0, h), x.W64)
+        S, z = x.gpu_state(state)
+        assert (np.abs(z[0, h] - zr) <= 7 * TOL * zr).all()
+        assert (np.abs(S[0, h] - Sr) <= 7 * TOL * np.abs(Sr).max(1, keepdims=True)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("factor", [2.0**-40, 2.0**30])
+def test_extend_values_of_any_size(cuda_device, dtype, factor):
+    x = Problem(1, 2, 600, 64, 256, dtype, cuda_device, prior=0, seed=12)
+    x.v *= factor
+    state = api.decode_extend(x.k, x.v, x.W, x.state)
+    status_ok()
+    check_state(x, state, [None])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_extend_values_that_grow_along_the_sequence(cuda_device, dtype):
+    """Value magnitudes 2^-30 .. 2^33 in one sequence, growing and falling."""
+    L = 1100
+    x = Problem(1, 2, L, 64, 128, dtype, cuda_device, prior=0, seed=13)
+    e = torch.linspace(-30, 33, L // 2, device=cuda_device).floor()
+    x.v *= torch.exp2(torch.cat([e, e.flip(0)]))[:, None].to(x.v.dtype)
+    state = api.decode_extend(x.k, x.v, x.W, x.state)
+    status_ok()
+    check_state(x, state, [None])
+
+
+def test_extend_then_step_continues_the_sequence(cuda_device):
+    """A prompt through decode_extend, then single tokens: the rows of the causal forward."""
+    from oracle import favor
+
+    L, n = 300, 8
+    x = Problem(1, 2, L + n, 64, 256, "f32", cuda_device, prior=0, seed=21)
+    state = api.decode_extend(x.k[:, :, :L].contiguous(), x.v[:, :, :L].contiguous(), x.W, x.state)
+    outs = [api.decode_step(*(y[:, :, t].contiguous() for y in (x.q, x.k, x.v)), x.W, state) for t in range(L, L + n)]
+    status_ok()
+    got = torch.stack(outs, 2).double().cpu().numpy()
+    ref = favor.fwd(*(y.double().cpu().numpy() for y in (x.q, x.k, x.v)), x.W64, causal=True)[:, :, L:]
+    assert rel_max_err(got, ref) <= TOL
+
+
+# ------------------------------------------------------------------------------------------- verify
+
+def draft(B, T, V, dtype, device, seed=0, spread=2.0):
+    g = np.random.default_rng(seed)
+    logits = g.standard_normal((B, T, V)) * spread
+    other = logits + g.standard_normal((B, T, V)) * 0.7
+    p, q = (torch.softmax(torch.tensor(a), -1).float() for a in (logits, other))
+    if dtype == "bf16":
+        p, q = p.to(torch.bfloat16), q.to(torch.bfloat16)
+    parents = random_parents(B, T, seed=seed, reach=4)
+    tokens = np.zeros((B, T), dtype=np.int64)
+    for b in range(B):
+        for c in range(1, T):
+            w = q[b, parents[b, c]].double().numpy()
+            tokens[b, c] = g.choice(V, p=w / w.sum())
+    u, r = g.random((B, T)).astype(np.float32), g.random(B).astype(np.float32)
+    return dict(parents=parents, tokens=tokens, p=p.to(device), q=q.to(device), u=u, r=r)
+
+
+def run_verify(x, device, dense=True, n_nodes=None):
+    got = api.decode_verify(i32(x["parents"], device), i32(x["tokens"], device), x["p"],
+                            torch.tensor(x["u"], device=device), torch.tensor(x["r"], device=device),
+                            q=x["q"] if dense else None,
+                            n_nodes=None if n_nodes is None else i32(n_nodes, device))
+    return [t.cpu().numpy() for t in got]
+
+
+def check_verify(x, got, dense=True, n_nodes=None):
+    path, count, token = got
+    B, T = path.shape
+    for b in range(B):
+        n = T if n_nodes is None else n_nodes[b]
+        if n == 0:
+            assert count[b] == 0 and token[b] == -1 and (path[b] == -1).all()
+            continue
+        ref, nxt = speculative.verify(x["parents"][b][:n], x["tokens"][b], x["p"][b].double().cpu().numpy(),
+                                      x["q"][b].double().cpu().numpy() if dense else None,
+                                      x["u"][b].astype(np.float64), float(x["r"][b]))
+        assert path[b].tolist() == ref + [-1] * (T - len(ref)) and count[b] == len(ref)
+        assert token[b] == nxt
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dense", [True, False])
+@pytest.mark.parametrize("B,T,V", [(1, 1, 1), (3, 2, 5), (2, 8, 31), (9, 16, 257), (1, 8, 32000), (4, 12, 5003),
+                                   (24, 128, 1001), (2, 3, 131072), (70, 20, 640)])
+def test_verify_matches_oracle(cuda_device, dtype, dense, B, T, V):
+    x = draft(B, T, V, dtype, cuda_device, seed=B + T)
+    got = run_verify(x, cuda_device, dense)
+    status_ok()
+    check_verify(x, got, dense)
+
+
+@pytest.mark.parametrize("dense", [True, False])
+def test_verify_ragged(cuda_device, dense):
+    x = draft(12, 24, 999, "f32", cuda_device, seed=5)
+    counts = [0, 1, 2, 24, 7, 0, 24, 12, 3, 23, 5, 1]
+    for b, n in enumerate(counts):  # nothing behind a sequence's nodes is looked at
+        x["parents"][b, n:], x["tokens"][b, n:], x["p"][b, n:] = 10**6, -(10**6), float("nan")
+    got = run_verify(x, cuda_device, dense, counts)
+    status_ok()
+    check_verify(x, got, dense, counts)
+
+
+@pytest.mark.parametrize("dense", [True, False])
+def test_verify_all_siblings_and_chains(cuda_device, dense):
+    """Many rejections at one node (repeated tokens among the siblings), and a chain accepted whole."""
+    T, V = 60, 700
+    x = draft(6, T, V, "f32", cuda_device, seed=6, spread=0.5)
+    x["parents"][:3] = np.where(np.arange(T) > 0, 0, -1)
+    x["u"][:3] = 0.9999
+    x["tokens"][:3] %= 40
+    x["parents"][3:] = np.arange(T) - 1
+    x["u"][3:] = 0.0
+    got = run_verify(x, cuda_device, dense)
+    status_ok()
+    check_verify(x, got, dense)
+    assert (got[1][3:] == T).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_verify_sample_numbers_at_their_ends(cuda_device, dtype):
+    x = draft(8, 1, 4000, dtype, cuda_device, seed=7)
+    x["p"][:, :, :9] = 0
+    x["p"][:, :, 3990:] = 0
+    x["r"][:] = [0.0, 1 - 2.0**-24, 2.0**-30, 0.5, 0.999999, 1e-6, 0.25, 0.75]
+    got = run_verify(x, cuda_device, False)
+    status_ok()
+    check_verify(x, got, False)
+    assert got[2][0] == 9 and (got[2] >= 9).all() and (got[2] < 3990).all()
+
+
+def test_verify_degenerate_rows(cuda_device):
+    """A draft equal to the target leaves no residual: the target's own row is sampled. One-hot targets
+    (greedy decoding). Rows without a positive sum answer -1 and are recorded."""
+    x = draft(4, 3, 500, "f32", cuda_device, seed=8)
+    x["q"] = x["p"].clone()
+    x["u"][:] = 1.0  # a number outside [0, 1): rejects a draft equal to the target
+    got = run_verify(x, cuda_device)
+    status_ok()
+    check_verify(x, got)
+    hot = torch.zeros_like(x["p"])
+    hot[:, :, 123] = 1
+    x["p"], x["u"][:] = hot, 0.3
+    x["tokens"][:, 1:] = 123
+    for dense in (True, False):
+        got = run_verify(x, cuda_device, dense)
+        status_ok()
+        check_verify(x, got, dense)
+        assert (got[2] == 123).all() and (got[1] > 1).all()
+    for bad in (0.0, float("nan"), float("inf"), -1.0):
+        x["p"] = torch.full_like(hot, bad)
+        x["parents"][:] = -1
+        got = run_verify(x, cuda_device)
+        assert api.sync_status() == api.FAVOR_ERR_INVALID_ARG
+        assert (got[2] == -1).all() and (got[1] == 1).all()
+    status_ok()
+
+
+def test_verify_bad_parents_and_tokens_are_recorded(cuda_device):
+    x = draft(3, 10, 300, "f32", cuda_device, seed=9)
+    x["u"][:] = 0.0  # whatever can be accepted is
+    ref = {k: (v.copy() if isinstance(v, np.ndarray) else v) for k, v in x.items()}
+    x["parents"][0, 1], ref["parents"][0, 1] = 5, -1
+    x["tokens"][1, 1], ref["parents"][1, 1] = 300, -1
+    x["tokens"][2, 2], ref["parents"][2, 2] = -4, -1
+    got = run_verify(x, cuda_device)
+    assert api.sync_status() == api.FAVOR_ERR_INVALID_ARG
+    check_verify(ref, got)
+    status_ok()
+
+
+# ------------------------------------------------------------------------------------ used together
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_round_of_speculative_decoding(cuda_device, dtype):
+    """Prompt into the state, a drafted tree answered over it, the walk, and the accepted path added --
+    without a copy to the host. The state then holds the prompt and the path, and the accepted nodes'
+    rows are those of single steps over them."""
+    B, H, L, T, d, m, V = 3, 2, 90, 20, 64, 256, 400
+    x = Problem(B, H, T, d, m, dtype, cuda_device, prior=L, seed=30)
+    state = api.decode_extend(x.prior[1], x.prior[2], x.W, api.decode_state(B, H, d, m, cuda_device))
+    y = draft(B, T, V, "f32", cuda_device, seed=31)
+    parents, tokens = i32(y["parents"], cuda_device), i32(y["tokens"], cuda_device)
+    u, r = (torch.tensor(y[k] * 0.6, device=cuda_device) for k in "ur")
+    for _ in range(2):  # two rounds with the same drafts
+        out = api.decode_tree(x.q, x.k, x.v, x.W, state, parents)
+        path, n_path, token = api.decode_verify(parents, tokens, y["p"], u, r, q=y["q"])
+        before = state.clone()
+        api.decode_extend(x.k, x.v, x.W, state, index=path, counts=n_path)
+        for b in range(B):
+            cur = before.clone()
+            nodes = path[b, : n_path[b]].tolist()
+            for j in nodes:
+                o = api.decode_step(*(t[:, :, j].contiguous() for t in (x.q, x.k, x.v)), x.W, cur)
+                assert rel_max_err(out[b, :, j].double().cpu().numpy(), o[b].double().cpu().numpy()) <= TOL
+            a, c = (s.view(B, H, d + 2, m)[b].double().cpu().numpy() for s in (state, cur))
+            assert np.abs(a - c).max() <= TOL * np.abs(c).max()
+    status_ok()
+    assert int(n_path.max()) > 1
+
+
+def test_another_stream_and_captured_graphs(cuda_device):
+    """The calls on a side stream, and captured into two graphs that are replayed in turn: the same bits
+    as eager calls."""
+    B, H, T, V = 2, 3, 30, 3000
+    x = Problem(B, H, T, 64, 256, "bf16", cuda_device, seed=40)
+    long = Problem(1, 2, 1000, 64, 256, "bf16", cuda_device, seed=41)
+    y = draft(B, T, V, "f32", cuda_device, seed=42)
+    parents, tokens = i32(y["parents"], cuda_device), i32(y["tokens"], cuda_device)
+    u, r = (torch.tensor(y[k], device=cuda_device) for k in "ur")
+    base, base_long = x.state.clone(), long.state.clone()
+
+    def decode():
+        out = api.decode_tree(x.q, x.k, x.v, x.W, x.state, parents)
+        path, n, token = api.decode_verify(parents, tokens, y["p"], u, r, q=y["q"])
+        api.decode_extend(x.k, x.v, x.W, x.state, index=path, counts=n)
+        return out, path, n, token, x.state
+
+    def prompt():
+        return (api.decode_extend(long.k, long.v, long.W, long.state),)
+
+    def eager(f, state, start):
+        state.copy_(start)
+        return [t.clone() for t in f()]
+
+    want = eager(decode, x.state, base), eager(prompt, long.state, base_long)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = eager(decode, x.state, base), eager(prompt, long.state, base_long)
+    torch.cuda.current_stream().wait_stream(side)
+    for a, b in zip(want, got):
+        assert all(torch.equal(s, t) for s, t in zip(a, b))
+    graphs, outs = [], []
+    for f in (decode, prompt):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(f())
+        graphs.append(g)
+    for _ in range(2):
+        x.state.copy_(base)
+        long.state.copy_(base_long)
+        for g in graphs:
+            g.replay()
+        for a, b in zip(want, outs):
+            assert all(torch.equal(s, t) for s, t in zip(a, b))
+    status_ok()
+
+
+def test_binding_refuses_what_does_not_fit(cuda_device):
+    x = Problem(2, 2, 6, 64, 128, "bf16", cuda_device, prior=0)
+    parents = i32(random_parents(2, 6), cuda_device)
+    p = torch.full((2, 6, 10), 0.1, device=cuda_device)
+    u, r = torch.zeros(2, 6, device=cuda_device), torch.zeros(2, device=cuda_device)
+    tree = [x.q, x.k, x.v, x.W, x.state, parents]
+
+    def put(args, i, t):
+        return args[:i] + [t] + args[i + 1:]
+
+    calls = [lambda a=put(tree, i, t): api.decode_tree(*a) for i, t in
+             [(1, x.k[:, :, :3].contiguous()), (2, x.v.float()), (3, x.W[:, :32].contiguous()), (4, x.state[:-1]),
+              (4, x.state.half()), (5, parents.long()), (5, parents[:, :5].contiguous()), (5, parents.cpu()),
+              (0, x.q.transpose(1, 2)), (5, parents.t().contiguous().t())]]
+    calls += [lambda: api.decode_tree(*tree, n_nodes=parents), lambda: api.decode_tree(*tree, out=x.q),
+              lambda: api.decode_extend(x.k, x.v, x.W, x.state, index=parents[0]),
+              lambda: api.decode_extend(x.k, x.v, x.W, x.state, index=parents[:, :0]),
+              lambda: api.decode_extend(x.k, x.v, x.W, x.state, counts=parents),
+              lambda: api.decode_extend(x.k, x.v, x.W, x.state[2:]),
+              lambda: api.decode_verify(parents, parents, p, u, r, q=p[:, :, :9].contiguous()),
+              lambda: api.decode_verify(parents, parents, p, u, r, q=p.bfloat16()),
+              lambda: api.decode_verify(parents, parents, p, u.double(), r),
+              lambda: api.decode_verify(parents, parents, p, u, u),
+              lambda: api.decode_verify(parents, parents, p.half(), u, r),
+              lambda: api.decode_verify(parents, parents[:1], p, u, r)]
+    for i, call in enumerate(calls):
+        with pytest.raises(api.FavorError) as e:
+            call()
+        assert e.value.status == api.FAVOR_ERR_INVALID_ARG, i
+    status_ok()
