@@ -286,8 +286,8 @@ FAVOR_API size_t favor_decode_extend_workspace_size(const favor_shape *shape, in
  *   index        : device, int32 [B,n_index]: the positions (0 .. L-1) of the tokens to add; one named
  *                  twice is added twice, one out of range not at all. NULL (n_index = 0): 0, 1, ...
  *   counts       : device, int32 [B]: how many of them, 0 .. n_index (0 .. L without index), clamped; a
- *                  sequence with 0 keeps its state bit for bit. NULL: all. k, v and index behind the
- *                  count are not read.
+ *                  sequence with 0 keeps its state bit for bit. NULL: all. What k, v and index hold behind
+ *                  the count does not matter.
  *   state        : device, favor_decode_state_size bytes, updated in place (all zeros: empty)
  *   workspace    : device, >= favor_decode_extend_workspace_size bytes, 256-B aligned
  *   stream       : cudaStream_t as void*

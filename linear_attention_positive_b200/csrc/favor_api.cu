@@ -23,6 +23,7 @@
 #include "k_decode.cu"
 #include "k_decode_tree.cu"
 #include "k_decode_extend.cu"
+#include "k_decode_extend_tc.cu"
 #include "k_decode_verify.cu"
 
 namespace favor {
@@ -1105,19 +1106,30 @@ bool decode_supported(const favor_shape *s) {
     return (s->d == 64 || s->d == 128) && s->m % 32 == 0 && s->m <= 256 && (long long)s->B * s->H <= 65535;
 }
 
-// Runs of tokens per head of favor_decode_extend, and tokens per run. Up to kExtWhole tokens (an
-// accepted path, a short prompt) the state is updated in place by one CTA a head; longer inputs are
-// cut so that about four CTAs an SM are in flight.
+// How favor_decode_extend takes n_tok tokens a head: on tensor cores (bf16 in order) or CUDA cores,
+// and the runs each head is cut into.
+//   CUDA cores: up to kExtWhole tokens (an accepted path, a short prompt) one CTA a head updates the
+//   state in place; more are cut so that about four CTAs an SM are in flight.
+//   Tensor cores: as many runs of whole tiles as fill two CTAs an SM once.
 constexpr int kExtWhole = 32;
+constexpr int kExtTcMin = 64;
 struct ExtendPlan {
+    bool tc;
     int n_split, tok_per_split;
 };
-ExtendPlan extend_plan(const favor_shape *s, int n_tok) {
-    if (n_tok <= kExtWhole) return {1, n_tok};
-    const long long BH = (long long)s->B * s->H, ctas = 4ll * num_sms();
+ExtendPlan extend_plan(const favor_shape *s, int n_tok, bool indexed) {
+    const long long BH = (long long)s->B * s->H;
+    if (s->dtype == FAVOR_BF16 && !indexed && n_tok >= kExtTcMin) {
+        const long long nt = (n_tok - 1) / kTile + 1, rows = BH * ((s->m + 127) / 128);
+        const long long runs = std::max<long long>(1, std::min(nt, 2ll * num_sms() / rows));
+        const long long per = (nt + runs - 1) / runs;
+        return {true, (int)((nt + per - 1) / per), (int)(per * kTile)};
+    }
+    if (n_tok <= kExtWhole) return {false, 1, n_tok};
+    const long long ctas = 4ll * num_sms();
     long long per = std::max<long long>(kExtWhole, (BH * n_tok + ctas - 1) / ctas);
     per = std::min<long long>((per + kExtTok - 1) / kExtTok * kExtTok, n_tok);
-    return {(int)((n_tok + per - 1) / per), (int)per};
+    return {false, (int)((n_tok + per - 1) / per), (int)per};
 }
 
 }  // namespace
@@ -1139,7 +1151,7 @@ extern "C" favor_status favor_decode_tree(const favor_shape *s, const void *q, c
 
 extern "C" size_t favor_decode_extend_workspace_size(const favor_shape *s, int n_index) {
     if (!shape_ok(s) || n_index < 0 || !decode_supported(s)) return 0;
-    const ExtendPlan pl = extend_plan(s, n_index > 0 ? n_index : s->L);
+    const ExtendPlan pl = extend_plan(s, n_index > 0 ? n_index : s->L, n_index > 0);
     if (pl.n_split == 1) return 256;
     return align256((size_t)s->B * s->H * pl.n_split * ((size_t)s->d * s->m + 2 * s->m) * 4);
 }
@@ -1157,10 +1169,15 @@ extern "C" favor_status favor_decode_extend(const favor_shape *s, const void *k,
         ws_bytes < favor_decode_extend_workspace_size(s, n_index))
         return FAVOR_ERR_WORKSPACE;
     const int n_tok = n_index > 0 ? n_index : s->L;
-    const ExtendPlan pl = extend_plan(s, n_tok);
+    const ExtendPlan pl = extend_plan(s, n_tok, n_index > 0);
     ExtendParams p{s->B, s->H, s->L, s->m, s->dtype == FAVOR_BF16 ? 1 : 0, k, v, W, index, counts, n_tok, state,
                    (float *)workspace, pl.n_split, pl.tok_per_split};
-    return cuda_status(launch_decode_extend(p, s->d, (cudaStream_t)stream));
+    if (!pl.tc) return cuda_status(launch_decode_extend(p, s->d, (cudaStream_t)stream));
+    CUtensorMap mK, mV, mW;
+    if (!make_token_map(&mK, k, s->B * s->H, s->L, s->d) || !make_token_map(&mV, v, s->B * s->H, s->L, s->d) ||
+        !make_w_map(&mW, W, s->m, s->d, 128))
+        return FAVOR_ERR_CUDA;
+    return cuda_status(launch_decode_extend_tc(mK, mV, mW, p, s->d, (cudaStream_t)stream));
 }
 
 extern "C" favor_status favor_decode_verify(const favor_verify_shape *s, const int *parents, const int *tokens,

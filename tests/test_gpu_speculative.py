@@ -237,6 +237,23 @@ def test_extend_matches_oracle(cuda_device, dtype, prior, B, H, L, d, m):
     assert torch.equal(again, state)
 
 
+@pytest.mark.parametrize("L,d,m", [(1300, 64, 256), (1300, 128, 256), (1153, 64, 96), (640, 128, 128), (257, 64, 128)])
+def test_extend_runs_of_many_tiles(cuda_device, L, d, m):
+    """Enough heads that each takes its tokens in one or two long runs (some heads checked)."""
+    B, H = 20, 16
+    x = Problem(B, H, L, d, m, "bf16", cuda_device, prior=0, seed=L)
+    counts = np.random.default_rng(L).integers(0, L + 1, B)
+    counts[:3] = L, 0, L - 1
+    state = api.decode_extend(x.k, x.v, x.W, x.state, counts=i32(counts, cuda_device))
+    status_ok()
+    S, z = x.gpu_state(state)
+    for b, h in [(0, 0), (0, 15), (1, 7), (2, 3), (3, 1), (11, 9), (19, 15)]:
+        n = int(counts[b])
+        Sr, zr = speculative.decode_extend(np.zeros((m, d)), np.zeros(m), x.head(x.k, b, h)[:n], x.head(x.v, b, h)[:n], x.W64)
+        assert np.abs(S[b, h] - Sr).max() <= TOL * np.abs(Sr).max()
+        assert np.abs(z[b, h] - zr).max() <= TOL * np.abs(zr).max()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("L,d,m", [(64, 64, 256), (64, 128, 96), (2000, 64, 256), (700, 128, 128)])
 def test_extend_counts_and_padding(cuda_device, dtype, L, d, m):
