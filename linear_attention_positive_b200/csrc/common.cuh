@@ -484,6 +484,34 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&h)[1
         : "memory");
 }
 
+#define FAVOR_RW16(v)                                                                                       \
+    "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), \
+        "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+
+// Loads 16 consecutive fp32 columns of this thread's TMEM lane (warp-collective), and its wait.
+__device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, float (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld16(float (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : FAVOR_RW16(v)::"memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+    tmem_ld16_nowait(taddr, v);
+    tmem_wait_ld16(v);
+}
+
+// Stores 8 consecutive 32-bit columns of this thread's TMEM lane (warp-collective; not waited).
+__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&h)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7])
+                 : "memory");
+}
+
 // Stores 64 consecutive 32-bit columns of this thread's TMEM lane (warp-collective; not waited).
 __device__ __forceinline__ void tmem_st64(uint32_t taddr, const uint32_t (&h)[64]) {
     asm volatile(

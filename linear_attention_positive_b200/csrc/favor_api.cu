@@ -22,6 +22,7 @@
 #include "k_selftest.cu"
 #include "k_decode.cu"
 #include "k_decode_tree.cu"
+#include "k_decode_tree_tc.cu"
 #include "k_decode_extend.cu"
 #include "k_decode_extend_tc.cu"
 #include "k_decode_verify.cu"
@@ -353,6 +354,20 @@ bool make_w_map(CUtensorMap *map, const void *base, int m, int d, int rows = 0) 
     const cuuint32_t box[2] = {64, (cuuint32_t)(rows > 0 ? rows : m)};
     const cuuint32_t estr[2] = {1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Carried decoding state (fp32, [d m + 2 m] a head): its S' part as a 3-D map (m, d, BH) with
+// 32-feature boxes of all value columns, 128-byte swizzle.
+bool make_state_map(CUtensorMap *map, const void *base, int BH, int d, int m) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)m, (cuuint64_t)d, (cuuint64_t)BH};
+    const cuuint64_t strides[2] = {(cuuint64_t)m * 4, (cuuint64_t)(d + 2) * m * 4};
+    const cuuint32_t box[3] = {32, (cuuint32_t)d, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void *>(base), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1106,6 +1121,9 @@ bool decode_supported(const favor_shape *s) {
     return (s->d == 64 || s->d == 128) && s->m % 32 == 0 && s->m <= 256 && (long long)s->B * s->H <= 65535;
 }
 
+// Trees of at least this many bf16 nodes go to the tensor cores.
+constexpr int kTreeTcMin = 2;
+
 // How favor_decode_extend takes n_tok tokens a head: on tensor cores (bf16 in order) or CUDA cores,
 // and the runs each head is cut into.
 //   CUDA cores: up to kExtWhole tokens (an accepted path, a short prompt) one CTA a head updates the
@@ -1146,7 +1164,14 @@ extern "C" favor_status favor_decode_tree(const favor_shape *s, const void *q, c
         return FAVOR_ERR_INVALID_ARG;
     if (!decode_supported(s) || s->L > FAVOR_TREE_MAX_NODES) return FAVOR_ERR_UNSUPPORTED;
     TreeParams p{s->B, s->H, s->L, s->m, s->dtype == FAVOR_BF16 ? 1 : 0, q, k, v, W, state, parents, n_nodes, out};
-    return cuda_status(launch_decode_tree(p, s->d, (cudaStream_t)stream));
+    if (s->dtype != FAVOR_BF16 || s->L < kTreeTcMin) return cuda_status(launch_decode_tree(p, s->d, (cudaStream_t)stream));
+    const int BH = s->B * s->H, rows = s->L <= 64 ? 64 : 128;
+    CUtensorMap mQ, mK, mV, mW, mS;
+    if (!make_token_map(&mQ, q, BH, s->L, s->d, rows) || !make_token_map(&mK, k, BH, s->L, s->d, rows) ||
+        !make_token_map(&mV, v, BH, s->L, s->d, rows) || !make_w_map(&mW, W, s->m, s->d, 128) ||
+        !make_state_map(&mS, state, BH, s->d, s->m))
+        return FAVOR_ERR_CUDA;
+    return cuda_status(launch_decode_tree_tc(mQ, mK, mV, mW, mS, p, s->d, (cudaStream_t)stream));
 }
 
 extern "C" size_t favor_decode_extend_workspace_size(const favor_shape *s, int n_index) {

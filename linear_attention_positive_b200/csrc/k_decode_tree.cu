@@ -69,12 +69,34 @@ __device__ __forceinline__ int tree_parent(const int *parents, int i) {
     return p;
 }
 
-// w_r . x from global memory (one thread).
+// w_r . x from global memory (one thread; 16-byte loads).
 template <int D>
 __device__ float dot_global(const void *W, const void *x, int bf16, int r, size_t x0) {
-    float acc = 0.f;
-    for (int c = 0; c < D; ++c) acc = fmaf(ld_elem(W, bf16, (size_t)r * D + c), ld_elem(x, bf16, x0 + c), acc);
-    return acc;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    if (bf16) {
+        const uint4 *w = (const uint4 *)((const uint16_t *)W + (size_t)r * D), *y = (const uint4 *)((const uint16_t *)x + x0);
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+            const uint4 a = __ldg(w + i), c = __ldg(y + i);
+            const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                acc[j] = fmaf(__uint_as_float(u[j] << 16), __uint_as_float(v[j] << 16), acc[j]);
+                acc[j] = fmaf(__uint_as_float(u[j] & 0xFFFF0000u), __uint_as_float(v[j] & 0xFFFF0000u), acc[j]);
+            }
+        }
+    } else {
+        const float4 *w = (const float4 *)((const float *)W + (size_t)r * D), *y = (const float4 *)((const float *)x + x0);
+#pragma unroll 4
+        for (int i = 0; i < D / 4; ++i) {
+            const float4 a = __ldg(w + i), c = __ldg(y + i);
+            acc[0] = fmaf(a.x, c.x, acc[0]);
+            acc[1] = fmaf(a.y, c.y, acc[1]);
+            acc[2] = fmaf(a.z, c.z, acc[2]);
+            acc[3] = fmaf(a.w, c.w, acc[3]);
+        }
+    }
+    return (acc[0] + acc[1]) + (acc[2] + acc[3]);
 }
 
 // One output row in log space over its own visible terms (one warp; lanes over features, then over
