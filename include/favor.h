@@ -331,8 +331,8 @@ typedef struct {
  *                  where that has no finite positive sum either, or n_nodes is 0, it is -1
  *   stream       : cudaStream_t as void*
  * p and q 16-byte aligned, the others 4-byte. Sums and residuals are fp64; no result depends on the order
- * blocks run in. Returns FAVOR_ERR_INVALID_ARG, FAVOR_ERR_UNSUPPORTED (T above the limit, B above 65535),
- * FAVOR_ERR_CUDA.
+ * blocks run in. Returns FAVOR_ERR_INVALID_ARG, FAVOR_ERR_UNSUPPORTED (T above the limit, B above 65535,
+ * V above 2^30), FAVOR_ERR_CUDA.
  */
 FAVOR_API favor_status favor_decode_verify(const favor_verify_shape *shape, const int *parents, const int *tokens,
                                            const int *n_nodes, const void *p, const void *q, const float *u,

@@ -6,6 +6,7 @@ fallback).
 """
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -348,31 +349,61 @@ def decode_step(q, k, v, W, state, out=None, stream=None):
     return out
 
 
-def _check_like(name, t, shape, dtype, device):
-    """An argument beside the main tensors: contiguous, of this shape, type and device (None passes)."""
-    if t is None:
-        return
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+# The calls of a decoding round take a few microseconds on the device, so their checks are written to
+# cost little on the host: one pass over each tensor's attributes, shape structs reused by value, no
+# wrapper objects around pointers, and the device switched only where it is another than the current one.
+
+@functools.lru_cache(maxsize=256)
+def _shape_ref(cls, *dims):
+    """A reference to a shape struct of these values (structs are never written to)."""
+    return ctypes.byref(cls(*dims))
+
+
+def _fits(name, t, shape, dtype, device):
+    """Refuses an argument that is not contiguous or not of this shape, type and device."""
+    if t.dtype is not dtype or t.device != device or t.shape != shape or not t.is_contiguous():
         raise FavorError(FAVOR_ERR_INVALID_ARG,
                          f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
-def _check_tokens(first, rest, W, state):
-    """Token tensors [B,H,L,d] of one shape, W [m,d] and a carried state, on one CUDA device."""
-    _check_inputs((first, *rest, W), first)
-    if first.dim() != 4 or W.dim() != 2 or W.shape[1] != first.shape[3]:
-        raise FavorError(FAVOR_ERR_INVALID_ARG, "tokens must be [B,H,L,d] and W [m,d]")
-    for t in (*rest, W):
-        if t.device != first.device:
-            raise FavorError(FAVOR_ERR_INVALID_ARG, "tensors must be on one device")
-        if t is not W and t.shape != first.shape:
-            raise FavorError(FAVOR_ERR_INVALID_ARG, "token tensors must have one shape")
-    torch = _torch()
-    B, H, _, d = first.shape
+def _opt_ptr(name, t, shape, dtype, device):
+    """The address of an argument that may be None, checked."""
+    if t is None:
+        return None
+    _fits(name, t, shape, dtype, device)
+    return t.data_ptr()
+
+
+def _tokens(first, rest, W, state):
+    """Checks token tensors [B,H,L,d] of one shape, W [m,d] and a carried state on one CUDA device.
+    Returns (B, H, L, d, m, dtype code) and the device."""
+    if not first.is_cuda or first.dim() != 4 or W.dim() != 2:
+        raise FavorError(FAVOR_ERR_INVALID_ARG, "tokens must be contiguous CUDA tensors [B,H,L,d] and W [m,d]")
+    size, dtype, device = first.shape, first.dtype, first.device
+    B, H, L, d = size
     m = W.shape[0]
-    if not state.is_contiguous() or state.dtype != torch.float32 or state.device != first.device or \
-            state.numel() != B * H * (d + 2) * m:
+    _fits("tokens", first, size, dtype, device)
+    for t in rest:
+        _fits("tokens", t, size, dtype, device)
+    _fits("W", W, (m, d), dtype, device)
+    if state.dtype is not _torch().float32 or state.device != device or state.numel() != B * H * (d + 2) * m or \
+            not state.is_contiguous():
         raise FavorError(FAVOR_ERR_INVALID_ARG, "state must come from decode_state() for these B, H, d, m and device")
+    return (B, H, L, d, m, _dtype_code(first)), device
+
+
+def _launch(what, f, device, stream, *args):
+    """Calls an entry point whose last argument is the stream (default: the current one of the tensors'
+    device) with that device current."""
+    torch = _torch()
+    raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+    if torch._C._cuda_getDevice() == device.index:
+        st = f(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, raw)
+    if st != FAVOR_OK:
+        raise FavorError(st, what)
 
 
 def decode_tree(q, k, v, W, state, parents, n_nodes=None, out=None, stream=None):
@@ -382,19 +413,23 @@ def decode_tree(q, k, v, W, state, parents, n_nodes=None, out=None, stream=None)
     the fp32 output [B,H,T,d]; its rows from n_nodes[b] on are left as they were in ``out`` (undefined
     when ``out`` is None)."""
     torch = _torch()
-    _check_tokens(q, (k, v), W, state)
-    B, H, T, d = q.shape
-    _check_like("parents", parents, (B, T), torch.int32, q.device)
-    _check_like("n_nodes", n_nodes, (B,), torch.int32, q.device)
-    _check_like("out", out, q.shape, torch.float32, q.device)
-    shape = _shape_of(q, W)
-    with torch.cuda.device(q.device):
-        if out is None:
-            out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-        st = library().favor_decode_tree(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(W), _ptr(state),
-                                         _ptr(parents), _ptr(n_nodes), _ptr(out), _stream_ptr(stream))
-    _check(st, "favor_decode_tree")
+    dims, device = _tokens(q, (k, v), W, state)
+    i32 = torch.int32
+    _fits("parents", parents, (dims[0], dims[2]), i32, device)
+    nodes = _opt_ptr("n_nodes", n_nodes, (dims[0],), i32, device)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.float32, device=device)
+    else:
+        _fits("out", out, q.shape, torch.float32, device)
+    _launch("favor_decode_tree", library().favor_decode_tree, device, stream, _shape_ref(Shape, *dims), q.data_ptr(),
+            k.data_ptr(), v.data_ptr(), W.data_ptr(), state.data_ptr(), parents.data_ptr(), nodes, out.data_ptr())
     return out
+
+
+@functools.lru_cache(maxsize=256)
+def _extend_workspace(device_index, n_index, *dims):
+    """favor_decode_extend_workspace_size of a shape (it depends on the device's SM count too)."""
+    return library().favor_decode_extend_workspace_size(_shape_ref(Shape, *dims), n_index)
 
 
 def decode_extend(k, v, W, state, index=None, counts=None, workspace=None, stream=None):
@@ -403,25 +438,23 @@ def decode_extend(k, v, W, state, index=None, counts=None, workspace=None, strea
     to add (such as the path decode_verify returns) or None for all in order; counts: int32 [B] how many
     of them, or None."""
     torch = _torch()
-    _check_tokens(k, (v,), W, state)
-    B = k.shape[0]
-    if index is not None and (index.dim() != 2 or index.shape[1] == 0):
-        raise FavorError(FAVOR_ERR_INVALID_ARG, "index must be [B,N], N >= 1")
-    n_index = 0 if index is None else index.shape[1]
-    _check_like("index", index, (B, n_index), torch.int32, k.device)
-    _check_like("counts", counts, (B,), torch.int32, k.device)
-    shape = _shape_of(k, W)
-    lib = library()
-    with torch.cuda.device(k.device):
-        if workspace is None:
-            ws_n = lib.favor_decode_extend_workspace_size(ctypes.byref(shape), n_index)
-            if ws_n == 0:
-                raise FavorError(FAVOR_ERR_UNSUPPORTED, "favor_decode_extend_workspace_size")
-            workspace = _alloc_bytes(ws_n, k.device)
-        st = lib.favor_decode_extend(ctypes.byref(shape), _ptr(k), _ptr(v), _ptr(W), _ptr(index), n_index,
-                                     _ptr(counts), _ptr(state), _ptr(workspace), workspace.numel(),
-                                     _stream_ptr(stream))
-    _check(st, "favor_decode_extend")
+    dims, device = _tokens(k, (v,), W, state)
+    i32, n_index, index_ptr = torch.int32, 0, None
+    if index is not None:
+        if index.dim() != 2 or index.shape[1] == 0:
+            raise FavorError(FAVOR_ERR_INVALID_ARG, "index must be [B,N], N >= 1")
+        n_index = index.shape[1]
+        _fits("index", index, (dims[0], n_index), i32, device)
+        index_ptr = index.data_ptr()
+    n_tok = _opt_ptr("counts", counts, (dims[0],), i32, device)
+    if workspace is None:
+        ws_n = _extend_workspace(device.index, n_index, *dims)
+        if ws_n == 0:
+            raise FavorError(FAVOR_ERR_UNSUPPORTED, "favor_decode_extend_workspace_size")
+        workspace = torch.empty(ws_n, dtype=torch.uint8, device=device)
+    _launch("favor_decode_extend", library().favor_decode_extend, device, stream, _shape_ref(Shape, *dims),
+            k.data_ptr(), v.data_ptr(), W.data_ptr(), index_ptr, n_index, n_tok, state.data_ptr(),
+            workspace.data_ptr(), workspace.numel())
     return state
 
 
@@ -431,23 +464,22 @@ def decode_verify(parents, tokens, p, u, r, q=None, n_nodes=None, stream=None):
     fp32 [B,T], r: fp32 [B] uniform numbers in [0, 1). Returns (path [B,T], n_path [B], next_token [B]),
     int32: path and n_path go to decode_extend as index and counts."""
     torch = _torch()
-    _check_inputs((p,) if q is None else (p, q), p)
-    if p.dim() != 3:
-        raise FavorError(FAVOR_ERR_INVALID_ARG, "p must be [B,T,V]")
-    B, T, V = p.shape
-    _check_like("q", q, p.shape, p.dtype, p.device)
-    _check_like("parents", parents, (B, T), torch.int32, p.device)
-    _check_like("tokens", tokens, (B, T), torch.int32, p.device)
-    _check_like("n_nodes", n_nodes, (B,), torch.int32, p.device)
-    _check_like("u", u, (B, T), torch.float32, p.device)
-    _check_like("r", r, (B,), torch.float32, p.device)
-    shape = VerifyShape(B, T, V, _dtype_code(p))
-    with torch.cuda.device(p.device):
-        path, n_path, token = (torch.empty(s, dtype=torch.int32, device=p.device) for s in ((B, T), (B,), (B,)))
-        st = library().favor_decode_verify(ctypes.byref(shape), _ptr(parents), _ptr(tokens), _ptr(n_nodes), _ptr(p),
-                                           _ptr(q), _ptr(u), _ptr(r), _ptr(path), _ptr(n_path), _ptr(token),
-                                           _stream_ptr(stream))
-    _check(st, "favor_decode_verify")
+    if not p.is_cuda or p.dim() != 3:
+        raise FavorError(FAVOR_ERR_INVALID_ARG, "p must be a contiguous CUDA tensor [B,T,V]")
+    size, device, i32, f32 = p.shape, p.device, torch.int32, torch.float32
+    B, T, V = size
+    nodes, row = (B, T), (B,)
+    _fits("p", p, size, p.dtype, device)
+    draft = _opt_ptr("q", q, size, p.dtype, device)
+    _fits("parents", parents, nodes, i32, device)
+    _fits("tokens", tokens, nodes, i32, device)
+    used = _opt_ptr("n_nodes", n_nodes, row, i32, device)
+    _fits("u", u, nodes, f32, device)
+    _fits("r", r, row, f32, device)
+    path, n_path, token = parents.new_empty(nodes), parents.new_empty(row), parents.new_empty(row)
+    _launch("favor_decode_verify", library().favor_decode_verify, device, stream,
+            _shape_ref(VerifyShape, B, T, V, _dtype_code(p)), parents.data_ptr(), tokens.data_ptr(), used, p.data_ptr(),
+            draft, u.data_ptr(), r.data_ptr(), path.data_ptr(), n_path.data_ptr(), token.data_ptr())
     return path, n_path, token
 
 

@@ -1122,7 +1122,7 @@ bool decode_supported(const favor_shape *s) {
 }
 
 // Trees of at least this many bf16 nodes go to the tensor cores.
-constexpr int kTreeTcMin = 2;
+constexpr int kTreeTcMin = 5;
 
 // How favor_decode_extend takes n_tok tokens a head: on tensor cores (bf16 in order) or CUDA cores,
 // and the runs each head is cut into.
@@ -1216,7 +1216,7 @@ extern "C" favor_status favor_decode_verify(const favor_verify_shape *s, const i
     if (!aligned16(p) || !aligned16(q) || !aligned4(parents) || !aligned4(tokens) || !aligned4(n_nodes) ||
         !aligned4(u) || !aligned4(r) || !aligned4(path) || !aligned4(n_path) || !aligned4(next_token))
         return FAVOR_ERR_INVALID_ARG;
-    if (s->T > FAVOR_TREE_MAX_NODES || s->B > 65535) return FAVOR_ERR_UNSUPPORTED;
+    if (s->T > FAVOR_TREE_MAX_NODES || s->B > 65535 || s->V > 1 << 30) return FAVOR_ERR_UNSUPPORTED;
     VerifyParams a{s->B, s->T, s->V, parents, tokens, n_nodes, p, q, u, r, path, n_path, next_token};
     return cuda_status(launch_decode_verify(a, s->dtype == FAVOR_BF16, (cudaStream_t)stream));
 }

@@ -139,6 +139,98 @@ __global__ void __launch_bounds__(256) k_decode_extend_rows(ExtendParams p) {
     Dl[r] = Dr;
 }
 
+// ------------------------------------------------------------------------------- accepted paths
+//
+// Up to kExtPath tokens a head: one CTA per head, one thread per feature; all tokens' feature values
+// are formed first (registers), then the state streams through, kExtCols value columns in flight at a
+// time, each read, rescaled, added to and written once. Keeping S' out of the registers while the
+// features are formed lets four CTAs share an SM, which is what its loads need to reach HBM's rate; the
+// traffic, (m d + 2 m) * 8 bytes a head, is the bound.
+
+constexpr int kExtPath = 16;
+constexpr int kExtCols = 16;
+
+template <int D>
+__global__ void __launch_bounds__(256, 3) k_decode_extend_path(ExtendParams p) {
+    __shared__ __align__(16) float sK[kExtPath * D], sV[kExtPath * D];
+    __shared__ float sN[kExtPath];
+    const int bh = blockIdx.x, b = bh / p.H, m = p.m, r = threadIdx.x, warp = r >> 5, lane = r & 31, nw = m >> 5;
+    const int n = extend_count(p, b);
+    if (n == 0) return;  // the state stays as it is
+    float *S = p.state + (size_t)bh * ((size_t)D * m + 2 * m) + r;
+    float *z = S + (size_t)D * m, *Dl = z + m;
+    float zr = *z, Dr = *Dl, s[kExtCols];
+#pragma unroll
+    for (int c = 0; c < kExtCols; ++c) s[c] = S[(size_t)c * m];
+    const size_t row0 = (size_t)bh * p.L;
+    // a warp a token: gathered as fp32, half its squared norm with it (-1: not added)
+    for (int t = warp; t < kExtPath; t += nw) {
+        const int j = t < n ? extend_token(p, b, t) : -1;
+        float x = 0.f;
+        for (int c = lane; c < D; c += 32) {
+            const float k = j < 0 ? 0.f : ld_elem(p.k, p.bf16, (row0 + j) * D + c);
+            sK[t * D + c] = k;
+            sV[t * D + c] = j < 0 ? 0.f : ld_elem(p.v, p.bf16, (row0 + j) * D + c);
+            x = fmaf(k, k, x);
+        }
+        x = warp_sum(x);
+        if (lane == 0) sN[t] = j < 0 ? -1.f : 0.5f * x;
+    }
+    __syncthreads();
+    if (!(zr != 0.f)) Dr = -INFINITY;
+    float u[kExtPath], Dn = Dr;
+    {
+        float v[8];
+        feature_dots<D, 8>(p.W, p.bf16, r, sK, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = v[i], u[8 + i] = 0.f;
+        if (n > 8) {
+            feature_dots<D, 8>(p.W, p.bf16, r, sK + 8 * D, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[8 + i] = v[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kExtPath; ++i) {
+        u[i] = sN[i] < 0.f ? -INFINITY : u[i] - sN[i];
+        Dn = fmaxf(Dn, u[i]);
+    }
+    const float keep = zr != 0.f ? expf(Dr - Dn) : 0.f;
+    zr *= keep;
+#pragma unroll
+    for (int i = 0; i < kExtPath; ++i) {
+        u[i] = u[i] == -INFINITY ? 0.f : expf(u[i] - Dn);
+        zr += u[i];
+    }
+    if (zr != 0.f) {
+        *z = zr;
+        *Dl = Dn;
+    }
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += kExtCols) {
+        float x[kExtCols];
+#pragma unroll
+        for (int c = 0; c < kExtCols; ++c) {
+            x[c] = keep != 0.f ? s[c] * keep : 0.f;
+            if (c0 + kExtCols < D) s[c] = S[(size_t)(c0 + kExtCols + c) * m];
+        }
+#pragma unroll
+        for (int i = 0; i < kExtPath; ++i) {
+            if (i == 8 && n <= 8) break;
+#pragma unroll
+            for (int c = 0; c < kExtCols; c += 4) {
+                const float4 v = *(const float4 *)(sV + i * D + c0 + c);
+                ffma2(u[i], u[i], v.x, v.y, x[c], x[c + 1], x[c], x[c + 1]);
+                ffma2(u[i], u[i], v.z, v.w, x[c + 2], x[c + 3], x[c + 2], x[c + 3]);
+            }
+        }
+        if (zr != 0.f) {  // else no token entered this feature
+#pragma unroll
+            for (int c = 0; c < kExtCols; ++c) S[(size_t)(c0 + c) * m] = x[c];
+        }
+    }
+}
+
 // Adds the partial states of a head's runs (the first holds the carried state) into the state: one
 // thread per feature, kCombCols value columns per CTA; the CTA of the first columns writes z' and D.
 constexpr int kCombCols = 8;
@@ -175,6 +267,13 @@ __global__ void __launch_bounds__(256) k_extend_combine(ExtendParams p, int d) {
 
 cudaError_t launch_decode_extend(const ExtendParams &p, int d, cudaStream_t st) {
     const int BH = p.B * p.H;
+    if (p.n_split == 1 && p.n_tok <= kExtPath) {
+        if (d == 64)
+            k_decode_extend_path<64><<<BH, p.m, 0, st>>>(p);
+        else
+            k_decode_extend_path<128><<<BH, p.m, 0, st>>>(p);
+        return cudaGetLastError();
+    }
     if (d == 64)
         k_decode_extend_rows<64><<<dim3(p.n_split, BH), p.m, 0, st>>>(p);
     else

@@ -344,16 +344,24 @@ __global__ void __launch_bounds__(kTreeThreads) k_decode_tree_rows(TreeParams p)
         for (int k = 0; k < 8; ++k)
 #pragma unroll
             for (int t = 0; t < TQ; ++t) breg[k][t] = k < kk ? sB[(size_t)t * m + lane + 32 * k] : 0.f;
+        // a column's entries; those of the next state column are asked for one column ahead
+        auto state_col = [&](int col, float(&x)[8]) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = k < kk && col < D ? __ldg(S + (size_t)col * m + lane + 32 * k) : 0.f;
+        };
+        float ahead[8];
+        state_col(warp, ahead);
         for (int col = warp; col < D + 1 + nk; col += nw) {
             float x[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const int f = lane + 32 * k;
                 x[k] = k >= kk      ? 0.f
-                       : col < D    ? S[(size_t)col * m + f] * sS[f]
+                       : col < D    ? ahead[k] * sS[f]
                        : col == D   ? sZ[f]
                                     : sA[(size_t)(col - D - 1) * m + f];
             }
+            state_col(col + nw, ahead);
             float y[TQ];
 #pragma unroll
             for (int t = 0; t < TQ; ++t) y[t] = 0.f;
@@ -395,6 +403,169 @@ __global__ void __launch_bounds__(kTreeThreads) k_decode_tree_rows(TreeParams p)
         if (!(sC[2 * t + 1] >= kTreeDenMin)) tree_row_exact<D>(p, bh, i0 + t, sPar);
 }
 
+// ---------------------------------------------------------------------------- few nodes (T <= 8)
+//
+// One CTA per (head, 64 value columns), one thread per feature, all nodes at once, fp32 throughout. The
+// thread's 64 entries of S' are asked for before anything else and arrive under the projections; sums
+// over features are halving exchanges inside each warp, then across warps through shared memory. Small
+// trees are bound by the latency of that one chain: about 1 us for the loads and as much for the rest.
+
+constexpr int kFewCols = 64;
+
+// Sums of 64 per-lane values over the warp: on return lane l holds the sums of values 2 l, 2 l + 1.
+__device__ __forceinline__ void halving_sum64(float (&v)[64], int lane) {
+#pragma unroll
+    for (int o = 16, n = 64; o > 0; o >>= 1, n >>= 1) {
+        const bool up = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < n / 2; ++i) {
+            const float send = up ? v[i] : v[n / 2 + i];
+            const float keep = up ? v[n / 2 + i] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    }
+}
+
+template <int D, int TT>
+struct FewSmem {
+    static constexpr int LD = kFewCols + TT + 1;  // a row's sums: value columns, keys, normaliser
+    // floats: keys then queries [2 TT][D], values [TT][64], warps' sums [nw][TT][LD], sums [TT][LD], maxima, scales
+    __host__ __device__ static size_t bytes(int m) {
+        return 4 * ((size_t)2 * TT * D + TT * kFewCols + (size_t)(m / 32 + 1) * TT * LD + 8 * (TT + 1) + 4 * TT) + 8 * TT;
+    }
+};
+
+template <int D, int TT>
+__global__ void __launch_bounds__(256, 1) k_decode_tree_few(TreeParams p) {
+    constexpr int LD = FewSmem<D, TT>::LD;
+    extern __shared__ __align__(16) float sm[];
+    const int bh = blockIdx.x, b = bh / p.H, m = p.m, T = p.T, c0 = blockIdx.y * kFewCols;
+    const int r = threadIdx.x, warp = r >> 5, lane = r & 31, nw = m >> 5;
+    const int n = tree_count(p.n_nodes, b, T);
+    if (n == 0) return;
+    float *sX = sm, *sV = sX + 2 * TT * D, *sPart = sV + TT * kFewCols, *sY = sPart + (size_t)nw * TT * LD;
+    float *sMax = sY + TT * LD, *sE = sMax + 8 * (TT + 1), *sC = sE + TT;  // sC: [TT][2], state's scale and denominator
+    int *sPar = (int *)(sC + 3 * TT);
+    uint32_t *sVis = (uint32_t *)(sPar + TT);
+    const size_t row0 = (size_t)bh * T * D;
+
+    const float *S = p.state + (size_t)bh * ((size_t)D * m + 2 * m);
+    const float zr = S[(size_t)D * m + r], Dr = S[(size_t)D * m + m + r];
+    float s[kFewCols];
+#pragma unroll
+    for (int c = 0; c < kFewCols; ++c) s[c] = __ldg(S + (size_t)(c0 + c) * m + r);
+    for (int i = r; i < TT * D; i += m) {
+        sX[i] = i < n * D ? ld_elem(p.k, p.bf16, row0 + i) : 0.f;
+        sX[TT * D + i] = i < n * D ? ld_elem(p.q, p.bf16, row0 + i) : 0.f;
+    }
+    for (int i = r; i < TT * kFewCols; i += m) {
+        const int j = i / kFewCols, c = i % kFewCols;
+        sV[i] = j < n ? ld_elem(p.v, p.bf16, row0 + (size_t)j * D + c0 + c) : 0.f;
+    }
+    if (r < n) sPar[r] = tree_parent(p.parents + (size_t)b * T, r);
+    __syncthreads();
+    if (r < n) {
+        uint32_t x = 0;
+        for (int j = r; j >= 0; j = sPar[j]) x |= 1u << j;
+        sVis[r] = x;
+    }
+    for (int t = warp; t < n; t += nw) {
+        float x = 0.f;
+#pragma unroll
+        for (int c = lane; c < D; c += 32) x = fmaf(sX[t * D + c], sX[t * D + c], x);
+        x = warp_sum(x);
+        if (lane == 0) sE[t] = -0.5f * x;
+    }
+    float u[2 * TT], E = -INFINITY;
+    feature_dots<D, 2 * TT>(p.W, p.bf16, r, sX, u);
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+        if (t < n && fabsf(u[t]) < INFINITY) E = fmaxf(E, u[t]);
+    if (E == -INFINITY) E = 0.f;
+    const float ds = zr != 0.f ? Dr - E : -INFINITY;
+#pragma unroll
+    for (int t = 0; t <= TT; ++t) {
+        const float x = warp_max(t < TT ? u[TT + t] + E : ds);
+        if (lane == 0) sMax[warp * (TT + 1) + t] = x;
+    }
+    __syncthreads();
+    float eS = sMax[TT];
+    for (int w = 1; w < nw; ++w) eS = fmaxf(eS, sMax[w * (TT + 1) + TT]);
+    const float sr = zr != 0.f ? expf(ds - eS) : 0.f;
+#pragma unroll
+    for (int c = 0; c < kFewCols; ++c) s[c] = sr != 0.f ? s[c] * sr : 0.f;
+#pragma unroll
+    for (int t = 0; t < TT; ++t) u[t] = expf(u[t] - E);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+        if (t < n) {
+            float f = sMax[t];
+            for (int w = 1; w < nw; ++w) f = fmaxf(f, sMax[w * (TT + 1) + t]);
+            const float bt = expf(u[TT + t] + E - f);
+            float *part = sPart + (size_t)(warp * TT + t) * LD;
+            float y[kFewCols], a[TT];
+#pragma unroll
+            for (int c = 0; c < kFewCols; ++c) y[c] = bt * s[c];
+            halving_sum64(y, lane);
+            part[2 * lane] = y[0];
+            part[2 * lane + 1] = y[1];
+#pragma unroll
+            for (int j = 0; j < TT; ++j) a[j] = bt * u[j];
+            halving_sum<TT>(a, lane);
+            if (lane % (32 / TT) == 0) part[kFewCols + lane / (32 / TT)] = a[0];
+            const float yz = warp_sum(bt * sr * zr);
+            if (lane == 0) part[kFewCols + TT] = yz;
+        }
+    }
+    __syncthreads();
+    for (int i = r; i < n * LD; i += m) {
+        float x = 0.f;
+        for (int w = 0; w < nw; ++w) x += sPart[(size_t)w * TT * LD + i];
+        sY[i] = x;
+    }
+    __syncthreads();
+    if (r < n) {  // the visible nodes' weights and the denominator
+        float *y = sY + r * LD, M = eS;
+        for (uint32_t x = sVis[r]; x != 0; x &= x - 1) M = fmaxf(M, sE[__ffs(x) - 1]);
+        const float cS = eS == -INFINITY ? 0.f : expf(eS - M);
+        float den = cS == 0.f ? 0.f : cS * y[kFewCols + TT];
+        for (uint32_t x = sVis[r]; x != 0; x &= x - 1) {
+            const int j = __ffs(x) - 1;
+            const float w = expf(sE[j] - M) * y[kFewCols + j];
+            y[kFewCols + j] = w;
+            den += w;
+        }
+        sC[2 * r] = cS;
+        sC[2 * r + 1] = den;
+    }
+    __syncthreads();
+    for (int i = r; i < n * kFewCols; i += m) {
+        const int t = i / kFewCols, c = i % kFewCols;
+        const float *y = sY + t * LD, cS = sC[2 * t], den = sC[2 * t + 1];
+        if (!(den >= kTreeDenMin)) continue;
+        float num = cS == 0.f ? 0.f : cS * y[c];
+        for (uint32_t x = sVis[t]; x != 0; x &= x - 1) {
+            const int j = __ffs(x) - 1;
+            num = fmaf(y[kFewCols + j], sV[j * kFewCols + c], num);
+        }
+        p.out[row0 + (size_t)t * D + c0 + c] = num / den;
+    }
+    if (c0 == 0)
+        for (int t = warp; t < n; t += nw)
+            if (!(sC[2 * t + 1] >= kTreeDenMin)) tree_row_exact<D>(p, bh, t, sPar);
+}
+
+template <int D, int TT>
+static cudaError_t launch_tree_few(const TreeParams &p, cudaStream_t st) {
+    const size_t sm = FewSmem<D, TT>::bytes(p.m);
+    if (sm > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(k_decode_tree_few<D, TT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+        if (e != cudaSuccess) return e;
+    }
+    k_decode_tree_few<D, TT><<<dim3(p.B * p.H, D / kFewCols), p.m, sm, st>>>(p);
+    return cudaGetLastError();
+}
+
 template <int D, int TQ>
 static cudaError_t launch_tree_rows(const TreeParams &p, cudaStream_t st) {
     const size_t sm = TreeSmem<D>::bytes(TQ, p.T, p.m);
@@ -406,8 +577,9 @@ static cudaError_t launch_tree_rows(const TreeParams &p, cudaStream_t st) {
 
 template <int D>
 static cudaError_t launch_decode_tree_d(const TreeParams &p, cudaStream_t st) {
-    if (p.T == 1) return launch_tree_rows<D, 1>(p, st);
-    if (p.T <= 4) return launch_tree_rows<D, 4>(p, st);
+    if (p.T == 1) return launch_tree_few<D, 1>(p, st);
+    if (p.T <= 4) return launch_tree_few<D, 4>(p, st);
+    if (p.T <= 8) return launch_tree_few<D, 8>(p, st);
     return launch_tree_rows<D, 16>(p, st);
 }
 
