@@ -541,6 +541,37 @@ __device__ __forceinline__ void ffma2(float a0, float a1, float b0, float b1, fl
     asm("mov.b64 {%0, %1}, %2;" : "=f"(r0), "=f"(r1) : "l"(r));
 }
 
+// D += A B for one warp: A 16 x 16 (row-major), B 16 x 8 (column-major), bf16 in, fp32 out. With
+// g = lane / 4, t = lane % 4: a0, a1 rows g, g + 8 at K = 2t, 2t + 1 and a2, a3 the same at K + 8; b0, b1
+// column g at K = 2t, 2t + 1 and K + 8; d0, d1 row g at columns 2t, 2t + 1 and d2, d3 row g + 8. (For
+// products of a few rows inside kernels bound by other things; tiles go to tcgen05.)
+__device__ __forceinline__ void mma_bf16_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                 uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same for tf32 operands, K = 8: a0, a1 rows g, g + 8 at K = t and a2, a3 at K = t + 4; b0, b1 column
+// g at K = t and t + 4.
+__device__ __forceinline__ void mma_tf32_16x8x8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// x as hi + lo, two tf32 values rounded to nearest: |x - hi - lo| <= 2^-22 |x|. (The tensor core drops the
+// low 13 bits; adding half of them first rounds.)
+__device__ __forceinline__ void tf32_split(float x, uint32_t &hi, uint32_t &lo) {
+    hi = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
+    lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
+}
+
 // Non-blocking test of an mbarrier phase (true once the phase with this parity has completed).
 __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
     uint32_t ok;

@@ -141,94 +141,126 @@ __global__ void __launch_bounds__(256) k_decode_extend_rows(ExtendParams p) {
 
 // ------------------------------------------------------------------------------- accepted paths
 //
-// Up to kExtPath tokens a head: one CTA per head, one thread per feature; all tokens' feature values
-// are formed first (registers), then the state streams through, kExtCols value columns in flight at a
-// time, each read, rescaled, added to and written once. Keeping S' out of the registers while the
-// features are formed lets four CTAs share an SM, which is what its loads need to reach HBM's rate; the
-// traffic, (m d + 2 m) * 8 bytes a head, is the bound.
+// Up to kExtPath tokens a head: one CTA per head, two features a thread. All tokens' feature values are
+// formed first (registers), then the state streams through, kExtCols value columns in flight at a time,
+// each read, rescaled, added to and written once; the traffic, (m d + 2 m) * 8 bytes a head, is the bound.
+// What has to stay out of its way is shared memory and L1 (one feature a thread, each reading its own
+// row of W and every value: 50 us for 1024 heads at d = 64, m = 256, with L1 77 % busy): two features
+// share each value read, and bf16 projections are warp MMAs, whose W fragments are 64-byte runs.
 
 constexpr int kExtPath = 16;
-constexpr int kExtCols = 16;
+constexpr int kExtCols = 8;
 
-template <int D>
-__global__ void __launch_bounds__(256, 3) k_decode_extend_path(ExtendParams p) {
-    __shared__ __align__(16) float sK[kExtPath * D], sV[kExtPath * D];
-    __shared__ float sN[kExtPath];
-    const int bh = blockIdx.x, b = bh / p.H, m = p.m, r = threadIdx.x, warp = r >> 5, lane = r & 31, nw = m >> 5;
+template <int D, bool BF16>
+__global__ void __launch_bounds__(128, 5) k_decode_extend_path(ExtendParams p) {
+    constexpr int LD = kExtPath + 1;
+    __shared__ __align__(16) float sV[kExtPath * D], sU[4 * 64 * LD];
+    __shared__ float sN[kExtPath];  // |k|^2 / 2, -1 for a token that is not added
+    const int bh = blockIdx.x, b = bh / p.H, m = p.m, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int n = extend_count(p, b);
     if (n == 0) return;  // the state stays as it is
-    float *S = p.state + (size_t)bh * ((size_t)D * m + 2 * m) + r;
+    const int nw = blockDim.x >> 5, f0 = 64 * warp;
+    const bool two = f0 + 32 < m;  // m is a multiple of 32: the last warp may have one feature a lane
+    float *S = p.state + (size_t)bh * ((size_t)D * m + 2 * m) + f0 + lane;
     float *z = S + (size_t)D * m, *Dl = z + m;
-    float zr = *z, Dr = *Dl, s[kExtCols];
+    const int second = two ? 32 : 0;  // (a lane without a second feature computes its first twice, stores it once)
+    float zr[2], Dr[2], s[2][kExtCols];
 #pragma unroll
-    for (int c = 0; c < kExtCols; ++c) s[c] = S[(size_t)c * m];
+    for (int h = 0; h < 2; ++h) {
+        zr[h] = z[h * second];
+        Dr[h] = Dl[h * second];
+    }
+    auto columns = [&](int c0) {
+#pragma unroll
+        for (int c = 0; c < kExtCols; ++c) {
+            s[0][c] = S[(size_t)(c0 + c) * m];
+            s[1][c] = S[(size_t)(c0 + c) * m + second];
+        }
+    };
+    columns(0);
     const size_t row0 = (size_t)bh * p.L;
-    // a warp a token: gathered as fp32, half its squared norm with it (-1: not added)
-    for (int t = warp; t < kExtPath; t += nw) {
-        const int j = t < n ? extend_token(p, b, t) : -1;
-        float x = 0.f;
-        for (int c = lane; c < D; c += 32) {
-            const float k = j < 0 ? 0.f : ld_elem(p.k, p.bf16, (row0 + j) * D + c);
-            sK[t * D + c] = k;
-            sV[t * D + c] = j < 0 ? 0.f : ld_elem(p.v, p.bf16, (row0 + j) * D + c);
-            x = fmaf(k, k, x);
-        }
-        x = warp_sum(x);
-        if (lane == 0) sN[t] = j < 0 ? -1.f : 0.5f * x;
+    for (int t = warp; t < n; t += nw) {  // a warp a value row
+        const int j = extend_token(p, b, t);
+        for (int c = lane; c < D; c += 32) sV[t * D + c] = j < 0 ? 0.f : ld_elem(p.v, BF16, (row0 + j) * D + c);
     }
+    for (int i = n * D + tid; i < kExtPath * D; i += blockDim.x) sV[i] = 0.f;
+    float u[2][kExtPath], *su = sU + warp * 64 * LD;
+    for (int t0 = 0; t0 < n; t0 += 8) {
+        const int t = t0 + (lane >> 2), j = t < n ? extend_token(p, b, t) : -1;
+        const void *x = j < 0 ? nullptr : (const char *)p.k + (row0 + j) * D * (BF16 ? 2 : 4);
+        const float sq = warp_logits<D, LD, 4, BF16>(p.W, m, f0, x, su, t0, lane);
+        if (warp == 0 && (lane & 3) == 0) sN[t] = j < 0 ? -1.f : 0.5f * sq;
+    }
+    if (n <= 8 && warp == 0 && lane < 8) sN[8 + lane] = -1.f;
     __syncthreads();
-    if (!(zr != 0.f)) Dr = -INFINITY;
-    float u[kExtPath], Dn = Dr;
-    {
-        float v[8];
-        feature_dots<D, 8>(p.W, p.bf16, r, sK, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = v[i], u[8 + i] = 0.f;
-        if (n > 8) {
-            feature_dots<D, 8>(p.W, p.bf16, r, sK + 8 * D, v);
+    for (int i = 0; i < kExtPath; ++i) {
+        u[0][i] = i < 8 || n > 8 ? su[lane * LD + i] : 0.f;
+        u[1][i] = i < 8 || n > 8 ? su[(lane + second) * LD + i] : 0.f;
+    }
+    float keep[2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) u[8 + i] = v[i];
+    for (int h = 0; h < 2; ++h) {
+        const bool old = zr[h] != 0.f;
+        float Dn = old ? Dr[h] : -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kExtPath; ++i) {
+            u[h][i] = sN[i] < 0.f ? -INFINITY : u[h][i] - sN[i];
+            Dn = fmaxf(Dn, u[h][i]);
         }
-    }
+        keep[h] = old ? expf(Dr[h] - Dn) : 0.f;
+        zr[h] *= keep[h];
 #pragma unroll
-    for (int i = 0; i < kExtPath; ++i) {
-        u[i] = sN[i] < 0.f ? -INFINITY : u[i] - sN[i];
-        Dn = fmaxf(Dn, u[i]);
-    }
-    const float keep = zr != 0.f ? expf(Dr - Dn) : 0.f;
-    zr *= keep;
-#pragma unroll
-    for (int i = 0; i < kExtPath; ++i) {
-        u[i] = u[i] == -INFINITY ? 0.f : expf(u[i] - Dn);
-        zr += u[i];
-    }
-    if (zr != 0.f) {
-        *z = zr;
-        *Dl = Dn;
+        for (int i = 0; i < kExtPath; ++i) {
+            u[h][i] = u[h][i] == -INFINITY ? 0.f : expf(u[h][i] - Dn);
+            zr[h] += u[h][i];
+        }
+        if (zr[h] != 0.f && (h == 0 || two)) {  // else no token entered this feature
+            z[h * second] = zr[h];
+            Dl[h * second] = Dn;
+        }
     }
 #pragma unroll 1
     for (int c0 = 0; c0 < D; c0 += kExtCols) {
-        float x[kExtCols];
+        float x[2][kExtCols];
 #pragma unroll
-        for (int c = 0; c < kExtCols; ++c) {
-            x[c] = keep != 0.f ? s[c] * keep : 0.f;
-            if (c0 + kExtCols < D) s[c] = S[(size_t)(c0 + kExtCols + c) * m];
-        }
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < kExtPath; ++i) {
-            if (i == 8 && n <= 8) break;
+            for (int c = 0; c < kExtCols; ++c) x[h][c] = keep[h] != 0.f ? s[h][c] * keep[h] : 0.f;
+        if (c0 + kExtCols < D) columns(c0 + kExtCols);
 #pragma unroll
-            for (int c = 0; c < kExtCols; c += 4) {
-                const float4 v = *(const float4 *)(sV + i * D + c0 + c);
-                ffma2(u[i], u[i], v.x, v.y, x[c], x[c + 1], x[c], x[c + 1]);
-                ffma2(u[i], u[i], v.z, v.w, x[c + 2], x[c + 3], x[c + 2], x[c + 3]);
+        for (int i0 = 0; i0 < kExtPath; i0 += 4) {
+            if (i0 < n) {
+#pragma unroll
+                for (int i = i0; i < i0 + 4; ++i)
+#pragma unroll
+                    for (int c = 0; c < kExtCols; c += 4) {
+                        const float4 v = *(const float4 *)(sV + i * D + c0 + c);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            ffma2(u[h][i], u[h][i], v.x, v.y, x[h][c], x[h][c + 1], x[h][c], x[h][c + 1]);
+                            ffma2(u[h][i], u[h][i], v.z, v.w, x[h][c + 2], x[h][c + 3], x[h][c + 2], x[h][c + 3]);
+                        }
+                    }
             }
         }
-        if (zr != 0.f) {  // else no token entered this feature
 #pragma unroll
-            for (int c = 0; c < kExtCols; ++c) S[(size_t)(c0 + c) * m] = x[c];
-        }
+        for (int h = 0; h < 2; ++h)
+            if (zr[h] != 0.f && (h == 0 || two)) {
+#pragma unroll
+                for (int c = 0; c < kExtCols; ++c) S[(size_t)(c0 + c) * m + h * second] = x[h][c];
+            }
     }
+}
+
+template <int D>
+static cudaError_t launch_extend_path(const ExtendParams &p, cudaStream_t st) {
+    const int threads = 32 * ((p.m + 63) / 64);
+    if (p.bf16)
+        k_decode_extend_path<D, true><<<p.B * p.H, threads, 0, st>>>(p);
+    else
+        k_decode_extend_path<D, false><<<p.B * p.H, threads, 0, st>>>(p);
+    return cudaGetLastError();
 }
 
 // Adds the partial states of a head's runs (the first holds the carried state) into the state: one
@@ -267,13 +299,7 @@ __global__ void __launch_bounds__(256) k_extend_combine(ExtendParams p, int d) {
 
 cudaError_t launch_decode_extend(const ExtendParams &p, int d, cudaStream_t st) {
     const int BH = p.B * p.H;
-    if (p.n_split == 1 && p.n_tok <= kExtPath) {
-        if (d == 64)
-            k_decode_extend_path<64><<<BH, p.m, 0, st>>>(p);
-        else
-            k_decode_extend_path<128><<<BH, p.m, 0, st>>>(p);
-        return cudaGetLastError();
-    }
+    if (p.n_tok <= kExtPath) return d == 64 ? launch_extend_path<64>(p, st) : launch_extend_path<128>(p, st);
     if (d == 64)
         k_decode_extend_rows<64><<<dim3(p.n_split, BH), p.m, 0, st>>>(p);
     else

@@ -226,6 +226,96 @@ __device__ __forceinline__ void feature_dots(const void *W, int bf16, int r, con
     }
 }
 
+// sU[f][t0 + g] = w_(f0 + f) . x_g for 16 MT of a warp's features and 8 tokens (x: this lane's token row
+// g, NULL for none; g = lane / 4); returns |x_g|^2. As warp MMAs: bf16 products are exact, fp32 rows are
+// hi + lo in tf32 (three products, 2^-22). K runs in the order in which 16-byte loads hand it out, the
+// same for both operands, so that W's fragments are 64-byte runs.
+template <int D, int LD, int MT, bool BF16>
+__device__ __forceinline__ float warp_logits(const void *Wv, int m, int f0, const void *xv, float *sU, int t0, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    float sq = 0.f;
+    if constexpr (BF16) {
+        const uint16_t *W = (const uint16_t *)Wv, *x = (const uint16_t *)xv;
+        uint4 xb[D / 32];
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+            xb[j] = x != nullptr ? __ldg((const uint4 *)(x + 32 * j + 8 * t)) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t u[4] = {xb[j].x, xb[j].y, xb[j].z, xb[j].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float lo = __uint_as_float(u[i] << 16), hi = __uint_as_float(u[i] & 0xFFFF0000u);
+                sq = fmaf(lo, lo, sq);
+                sq = fmaf(hi, hi, sq);
+            }
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            if (f0 + 16 * mt < m) {
+                const uint16_t *w = W + (size_t)(f0 + 16 * mt + g) * D + 8 * t;
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j) {
+                    const uint4 a = __ldg((const uint4 *)(w + 32 * j)), b = __ldg((const uint4 *)(w + 8 * D + 32 * j));
+                    mma_bf16_16x8x16(d, a.x, b.x, a.y, b.y, xb[j].x, xb[j].y);
+                    mma_bf16_16x8x16(d, a.z, b.z, a.w, b.w, xb[j].z, xb[j].w);
+                }
+                float *o = sU + (16 * mt + g) * LD + t0 + 2 * t;
+                o[0] = d[0];
+                o[1] = d[1];
+                o[8 * LD] = d[2];
+                o[8 * LD + 1] = d[3];
+            }
+        }
+    } else {
+        const float *W = (const float *)Wv, *x = (const float *)xv;
+        float d[MT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) d[mt][0] = d[mt][1] = d[mt][2] = d[mt][3] = 0.f;
+#pragma unroll 2
+        for (int j = 0; j < D / 16; ++j) {
+            const float4 b = x != nullptr ? __ldg((const float4 *)(x + 16 * j + 4 * t)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            sq += (b.x * b.x + b.y * b.y) + (b.z * b.z + b.w * b.w);
+            uint32_t bh[4], bl[4];
+            tf32_split(b.x, bh[0], bl[0]);
+            tf32_split(b.y, bh[1], bl[1]);
+            tf32_split(b.z, bh[2], bl[2]);
+            tf32_split(b.w, bh[3], bl[3]);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                if (f0 + 16 * mt < m) {
+                    const float *w = W + (size_t)(f0 + 16 * mt + g) * D + 16 * j + 4 * t;
+                    const float4 a0 = __ldg((const float4 *)w), a1 = __ldg((const float4 *)(w + 8 * D));
+                    const float a[2][4] = {{a0.x, a0.y, a0.z, a0.w}, {a1.x, a1.y, a1.z, a1.w}};
+                    uint32_t ah[2][4], al[2][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        tf32_split(a[0][i], ah[0][i], al[0][i]);
+                        tf32_split(a[1][i], ah[1][i], al[1][i]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2) {
+                        mma_tf32_16x8x8(d[mt], al[0][i], al[1][i], al[0][i + 1], al[1][i + 1], bh[i], bh[i + 1]);
+                        mma_tf32_16x8x8(d[mt], ah[0][i], ah[1][i], ah[0][i + 1], ah[1][i + 1], bl[i], bl[i + 1]);
+                        mma_tf32_16x8x8(d[mt], ah[0][i], ah[1][i], ah[0][i + 1], ah[1][i + 1], bh[i], bh[i + 1]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+            if (f0 + 16 * mt < m) {
+                float *o = sU + (16 * mt + g) * LD + t0 + 2 * t;
+                o[0] = d[mt][0];
+                o[1] = d[mt][1];
+                o[8 * LD] = d[mt][2];
+                o[8 * LD + 1] = d[mt][3];
+            }
+    }
+    sq += __shfl_xor_sync(0xffffffffu, sq, 1);
+    sq += __shfl_xor_sync(0xffffffffu, sq, 2);
+    return sq;
+}
+
 // Sums of TQ per-lane values over the warp: on return lane l holds in v[0] the sum of value
 // l * TQ / 32 (TQ <= 32, a power of two).
 template <int TQ>
@@ -429,9 +519,9 @@ __device__ __forceinline__ void halving_sum64(float (&v)[64], int lane) {
 template <int D, int TT>
 struct FewSmem {
     static constexpr int LD = kFewCols + TT + 1;  // a row's sums: value columns, keys, normaliser
-    // floats: keys then queries [2 TT][D], values [TT][64], warps' sums [nw][TT][LD], sums [TT][LD], maxima, scales
+    // floats: logits of keys and queries [m][17], values [TT][64], warps' sums [nw][TT][LD], sums [TT][LD], maxima, scales
     __host__ __device__ static size_t bytes(int m) {
-        return 4 * ((size_t)2 * TT * D + TT * kFewCols + (size_t)(m / 32 + 1) * TT * LD + 8 * (TT + 1) + 4 * TT) + 8 * TT;
+        return 4 * ((size_t)m * 17 + TT * kFewCols + (size_t)(m / 32 + 1) * TT * LD + 8 * (TT + 1) + 4 * TT) + 8 * TT;
     }
 };
 
@@ -443,7 +533,7 @@ __global__ void __launch_bounds__(256, 1) k_decode_tree_few(TreeParams p) {
     const int r = threadIdx.x, warp = r >> 5, lane = r & 31, nw = m >> 5;
     const int n = tree_count(p.n_nodes, b, T);
     if (n == 0) return;
-    float *sX = sm, *sV = sX + 2 * TT * D, *sPart = sV + TT * kFewCols, *sY = sPart + (size_t)nw * TT * LD;
+    float *sU = sm, *sV = sU + 17 * m, *sPart = sV + TT * kFewCols, *sY = sPart + (size_t)nw * TT * LD;
     float *sMax = sY + TT * LD, *sE = sMax + 8 * (TT + 1), *sC = sE + TT;  // sC: [TT][2], state's scale and denominator
     int *sPar = (int *)(sC + 3 * TT);
     uint32_t *sVis = (uint32_t *)(sPar + TT);
@@ -454,10 +544,6 @@ __global__ void __launch_bounds__(256, 1) k_decode_tree_few(TreeParams p) {
     float s[kFewCols];
 #pragma unroll
     for (int c = 0; c < kFewCols; ++c) s[c] = __ldg(S + (size_t)(c0 + c) * m + r);
-    for (int i = r; i < TT * D; i += m) {
-        sX[i] = i < n * D ? ld_elem(p.k, p.bf16, row0 + i) : 0.f;
-        sX[TT * D + i] = i < n * D ? ld_elem(p.q, p.bf16, row0 + i) : 0.f;
-    }
     for (int i = r; i < TT * kFewCols; i += m) {
         const int j = i / kFewCols, c = i % kFewCols;
         sV[i] = j < n ? ld_elem(p.v, p.bf16, row0 + (size_t)j * D + c0 + c) : 0.f;
@@ -469,15 +555,26 @@ __global__ void __launch_bounds__(256, 1) k_decode_tree_few(TreeParams p) {
         for (int j = r; j >= 0; j = sPar[j]) x |= 1u << j;
         sVis[r] = x;
     }
-    for (int t = warp; t < n; t += nw) {
-        float x = 0.f;
-#pragma unroll
-        for (int c = lane; c < D; c += 32) x = fmaf(sX[t * D + c], sX[t * D + c], x);
-        x = warp_sum(x);
-        if (lane == 0) sE[t] = -0.5f * x;
+    {
+        const size_t at = (row0 + (size_t)(lane >> 2) * D) * (p.bf16 ? 2 : 4);
+        const void *xk = (lane >> 2) < n ? (const char *)p.k + at : nullptr, *xq = xk ? (const char *)p.q + at : nullptr;
+        float sq;
+        if (p.bf16) {
+            sq = warp_logits<D, 17, 2, true>(p.W, m, 32 * warp, xk, sU + 32 * warp * 17, 0, lane);
+            warp_logits<D, 17, 2, true>(p.W, m, 32 * warp, xq, sU + 32 * warp * 17, 8, lane);
+        } else {
+            sq = warp_logits<D, 17, 2, false>(p.W, m, 32 * warp, xk, sU + 32 * warp * 17, 0, lane);
+            warp_logits<D, 17, 2, false>(p.W, m, 32 * warp, xq, sU + 32 * warp * 17, 8, lane);
+        }
+        if (warp == 0 && (lane & 3) == 0 && (lane >> 2) < TT) sE[lane >> 2] = -0.5f * sq;
     }
+    __syncwarp();
     float u[2 * TT], E = -INFINITY;
-    feature_dots<D, 2 * TT>(p.W, p.bf16, r, sX, u);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+        u[t] = sU[r * 17 + t];
+        u[TT + t] = sU[r * 17 + 8 + t];
+    }
 #pragma unroll
     for (int t = 0; t < TT; ++t)
         if (t < n && fabsf(u[t]) < INFINITY) E = fmaxf(E, u[t]);
