@@ -1121,8 +1121,13 @@ bool decode_supported(const favor_shape *s) {
     return (s->d == 64 || s->d == 128) && s->m % 32 == 0 && s->m <= 256 && (long long)s->B * s->H <= 65535;
 }
 
-// Trees of at least this many bf16 nodes go to the tensor cores.
-constexpr int kTreeTcMin = 5;
+// Whether a tree goes to the tensor cores' tiles (bf16). Up to 4 nodes the few-node kernel is faster at
+// any batch (1024 heads, d = 64, m = 256: 42 us against 87), up to 16 the row kernel while its CTAs fit
+// the SMs once (8 heads: 13 us against 18 at 8 nodes, 16 against 18 at 16; 1024 heads: 90 against 87).
+bool tree_on_tiles(const favor_shape *s) {
+    if (s->dtype != FAVOR_BF16 || s->L <= 4) return false;
+    return s->L > kRowsTile || (long long)s->B * s->H * (s->d / kRowsCols) > num_sms();
+}
 
 // How favor_decode_extend takes n_tok tokens a head: on tensor cores (bf16 in order) or CUDA cores,
 // and the runs each head is cut into.
@@ -1164,7 +1169,7 @@ extern "C" favor_status favor_decode_tree(const favor_shape *s, const void *q, c
         return FAVOR_ERR_INVALID_ARG;
     if (!decode_supported(s) || s->L > FAVOR_TREE_MAX_NODES) return FAVOR_ERR_UNSUPPORTED;
     TreeParams p{s->B, s->H, s->L, s->m, s->dtype == FAVOR_BF16 ? 1 : 0, q, k, v, W, state, parents, n_nodes, out};
-    if (s->dtype != FAVOR_BF16 || s->L < kTreeTcMin) return cuda_status(launch_decode_tree(p, s->d, (cudaStream_t)stream));
+    if (!tree_on_tiles(s)) return cuda_status(launch_decode_tree(p, s->d, (cudaStream_t)stream));
     const int BH = s->B * s->H, rows = s->L <= 64 ? 64 : 128;
     CUtensorMap mQ, mK, mV, mW, mS;
     if (!make_token_map(&mQ, q, BH, s->L, s->d, rows) || !make_token_map(&mK, k, BH, s->L, s->d, rows) ||

@@ -169,27 +169,6 @@ __device__ __noinline__ void tree_row_exact(const TreeParams &p, int bh, int i, 
     for (int c = 0; c < D / 32; ++c) p.out[row0 + (size_t)i * D + lane + 32 * c] = num[c] / den;
 }
 
-// ------------------------------------------------------------------------------- CUDA-core kernel
-//
-// One CTA per (head, tile of TQ rows), 256 threads, fp32 throughout. Feature phases: thread = feature
-// (W row streamed once per 16 tokens). Product phase: every column x over the features (the d state
-// columns, z', and a_j of the tile's and earlier nodes) is met by all TQ rows at once: a warp's lanes
-// hold b for their features and all rows in registers, read the column coalesced, and reduce the TQ
-// sums by a halving exchange.
-
-constexpr int kTreeThreads = 256;
-constexpr int kTreeTok = 16;  // tokens projected together
-
-template <int D>
-struct TreeSmem {
-    // floats: x tile, a [nk][m], b [TQ][m], y [TQ][D + 1 + T], s, s z, e [T], reductions
-    __host__ __device__ static size_t floats(int TQ, int T, int m) {
-        return (size_t)kTreeTok * D + (size_t)T * m + (size_t)TQ * m + (size_t)TQ * (D + 1 + T) + 2 * m + T + 8 * 16 + 16 +
-               TQ * 2;
-    }
-    __host__ __device__ static size_t bytes(int TQ, int T, int m) { return floats(TQ, T, m) * 4 + (size_t)T * 4; }
-};
-
 // acc[t] = w_r . x_t for NT tokens held in shared memory as fp32 rows.
 template <int D, int NT>
 __device__ __forceinline__ void feature_dots(const void *W, int bf16, int r, const float *sX, float (&acc)[NT]) {
@@ -334,166 +313,7 @@ __device__ __forceinline__ void halving_sum(float (&v)[TQ], int lane) {
     for (; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
 }
 
-template <int D, int TQ>
-__global__ void __launch_bounds__(kTreeThreads) k_decode_tree_rows(TreeParams p) {
-    extern __shared__ __align__(16) float sm[];
-    const int bh = blockIdx.x, b = bh / p.H, m = p.m, T = p.T;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nw = kTreeThreads / 32;
-    const int n = tree_count(p.n_nodes, b, T);
-    const int i0 = blockIdx.y * TQ;
-    if (i0 >= n) return;
-    const int rows = min(TQ, n - i0), nk = i0 + rows;  // ancestors come first: keys 0 .. nk-1
-    float *sX = sm, *sA = sX + kTreeTok * D, *sB = sA + (size_t)T * m, *sY = sB + (size_t)TQ * m;
-    const int ldy = D + 1 + T;
-    float *sS = sY + (size_t)TQ * ldy, *sZ = sS + m, *sE = sZ + m, *sRed = sE + T, *sTop = sRed + 8 * 16;
-    float *sC = sTop + 16;             // per row: e^(e_S - M), denominator
-    int *sPar = (int *)(sC + TQ * 2);
-    const size_t row0 = (size_t)bh * T * D;
-    for (int i = tid; i < nk; i += kTreeThreads) sPar[i] = tree_parent(p.parents + (size_t)b * T, i);
-
-    const float *S = p.state + (size_t)bh * ((size_t)D * m + 2 * m);
-    const int r = tid;
-    float zr = 0.f, Dr = 0.f, E = -INFINITY;
-    if (r < m) {
-        zr = S[(size_t)D * m + r];
-        Dr = S[(size_t)D * m + m + r];
-    }
-    // key logits
-    for (int j0 = 0; j0 < nk; j0 += kTreeTok) {
-        const int nt = min(kTreeTok, nk - j0);
-        __syncthreads();
-        for (int i = tid; i < kTreeTok * D; i += kTreeThreads)
-            sX[i] = i < nt * D ? ld_elem(p.k, p.bf16, row0 + (size_t)j0 * D + i) : 0.f;
-        __syncthreads();
-        for (int t = warp; t < nt; t += nw) {
-            float s = 0.f;
-            for (int c = lane; c < D; c += 32) s = fmaf(sX[t * D + c], sX[t * D + c], s);
-            s = warp_sum(s);
-            if (lane == 0) sE[j0 + t] = -0.5f * s;
-        }
-        if (r < m) {
-            float acc[kTreeTok];
-            feature_dots<D, kTreeTok>(p.W, p.bf16, r, sX, acc);
-#pragma unroll
-            for (int t = 0; t < kTreeTok; ++t)
-                if (t < nt) {
-                    sA[(size_t)(j0 + t) * m + r] = acc[t];
-                    if (fabsf(acc[t]) < INFINITY) E = fmaxf(E, acc[t]);
-                }
-        }
-    }
-    if (E == -INFINITY) E = 0.f;  // no finite logit
-    float ds = -INFINITY;
-    if (r < m) {
-        for (int j = 0; j < nk; ++j) sA[(size_t)j * m + r] = expf(sA[(size_t)j * m + r] - E);
-        if (zr != 0.f) ds = Dr - E;
-    }
-    const float dw = warp_max(ds);
-    if (lane == 0) sRed[warp] = dw;
-    __syncthreads();
-    float eS = sRed[0];
-    for (int w = 1; w < nw; ++w) eS = fmaxf(eS, sRed[w]);
-    if (r < m) {
-        const float s = zr != 0.f ? expf(ds - eS) : 0.f;
-        sS[r] = s;
-        sZ[r] = s * zr;
-    }
-    // query features of the tile's rows
-    for (int i = tid; i < TQ * D; i += kTreeThreads)
-        sX[i] = i < rows * D ? ld_elem(p.q, p.bf16, row0 + (size_t)i0 * D + i) : 0.f;
-    __syncthreads();
-    float uq[TQ];
-    if (r < m) {
-        feature_dots<D, TQ>(p.W, p.bf16, r, sX, uq);
-#pragma unroll
-        for (int t = 0; t < TQ; ++t) uq[t] += E;
-    } else {
-#pragma unroll
-        for (int t = 0; t < TQ; ++t) uq[t] = -INFINITY;
-    }
-#pragma unroll
-    for (int t = 0; t < TQ; ++t) {
-        const float mx = warp_max(uq[t]);
-        if (lane == 0) sRed[warp * 16 + t] = mx;
-    }
-    __syncthreads();
-    if (r < m) {
-#pragma unroll
-        for (int t = 0; t < TQ; ++t) {
-            float f = sRed[t];
-            for (int w = 1; w < nw; ++w) f = fmaxf(f, sRed[w * 16 + t]);
-            sB[(size_t)t * m + r] = expf(uq[t] - f);
-        }
-    }
-    __syncthreads();
-    // products of every column over the features with all rows
-    {
-        const int kk = m >> 5;
-        float breg[8][TQ];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-#pragma unroll
-            for (int t = 0; t < TQ; ++t) breg[k][t] = k < kk ? sB[(size_t)t * m + lane + 32 * k] : 0.f;
-        // a column's entries; those of the next state column are asked for one column ahead
-        auto state_col = [&](int col, float(&x)[8]) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = k < kk && col < D ? __ldg(S + (size_t)col * m + lane + 32 * k) : 0.f;
-        };
-        float ahead[8];
-        state_col(warp, ahead);
-        for (int col = warp; col < D + 1 + nk; col += nw) {
-            float x[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int f = lane + 32 * k;
-                x[k] = k >= kk      ? 0.f
-                       : col < D    ? ahead[k] * sS[f]
-                       : col == D   ? sZ[f]
-                                    : sA[(size_t)(col - D - 1) * m + f];
-            }
-            state_col(col + nw, ahead);
-            float y[TQ];
-#pragma unroll
-            for (int t = 0; t < TQ; ++t) y[t] = 0.f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-#pragma unroll
-                for (int t = 0; t < TQ; ++t) y[t] = fmaf(breg[k][t], x[k], y[t]);
-            halving_sum<TQ>(y, lane);
-            if (lane % (32 / TQ) == 0) sY[(size_t)(lane / (32 / TQ)) * ldy + col] = y[0];
-        }
-    }
-    __syncthreads();
-    // per row: the visible nodes' scales, the weights and the denominator
-    for (int t = tid; t < rows; t += kTreeThreads) {
-        float *y = sY + (size_t)t * ldy;
-        float M = eS;
-        for (int j = i0 + t; j >= 0; j = sPar[j]) M = fmaxf(M, sE[j]);
-        const float cS = eS == -INFINITY ? 0.f : expf(eS - M);
-        float den = cS == 0.f ? 0.f : cS * y[D];
-        for (int j = i0 + t; j >= 0; j = sPar[j]) {
-            const float w = expf(sE[j] - M) * y[D + 1 + j];
-            y[D + 1 + j] = w;
-            den += w;
-        }
-        sC[2 * t] = cS;
-        sC[2 * t + 1] = den;
-    }
-    __syncthreads();
-    for (int i = tid; i < rows * D; i += kTreeThreads) {
-        const int t = i / D, c = i - t * D;
-        const float *y = sY + (size_t)t * ldy;
-        const float cS = sC[2 * t], den = sC[2 * t + 1];
-        if (!(den >= kTreeDenMin)) continue;
-        float num = cS == 0.f ? 0.f : cS * y[c];
-        for (int j = i0 + t; j >= 0; j = sPar[j]) num = fmaf(y[D + 1 + j], ld_elem(p.v, p.bf16, row0 + (size_t)j * D + c), num);
-        p.out[row0 + (size_t)(i0 + t) * D + c] = num / den;
-    }
-    for (int t = warp; t < rows; t += nw)
-        if (!(sC[2 * t + 1] >= kTreeDenMin)) tree_row_exact<D>(p, bh, i0 + t, sPar);
-}
-
-// ---------------------------------------------------------------------------- few nodes (T <= 8)
+// ---------------------------------------------------------------------------- few nodes (T <= 4)
 //
 // One CTA per (head, 64 value columns), one thread per feature, all nodes at once, fp32 throughout. The
 // thread's 64 entries of S' are asked for before anything else and arrive under the projections; sums
@@ -663,12 +483,301 @@ static cudaError_t launch_tree_few(const TreeParams &p, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <int D, int TQ>
+// ------------------------------------------------------------------------- rows on warp MMAs
+//
+// One CTA per (head, tile of 16 rows, 64 value columns), 256 threads. Projections as warp MMAs with W's
+// fragments in registers; the products over the features, [16 rows x m] [m x (64 state columns + keys)],
+// as tf32 warp MMAs with both sides hi + lo (three products, 2^-22: fp32's precision), a group of 8
+// columns a warp. A warp's state columns are asked for before anything else. fp32 trees of any size,
+// and bf16 ones too small for whole tiles, where the latency of this chain (five barriers) is the bound.
+
+constexpr int kRowsThreads = 256;
+constexpr int kRowsTile = 16;
+constexpr int kRowsCols = 64;
+
+struct RowsSmem {
+    // floats: a [T][m + 16], b and b s [16][m + 16] each, values [T][64], sums [16][64 + T rounded up to 8],
+    // per feature E, D - E, z', per node e, parents and visible sets
+    __host__ __device__ static int ldy(int T) { return kRowsCols + (T + 7) / 8 * 8; }
+    __host__ __device__ static size_t floats(int T, int m) {
+        return (size_t)(T + 2 * kRowsTile) * (m + 16) + (size_t)T * kRowsCols + (size_t)kRowsTile * ldy(T) + 3 * m + T + 8 + 4 * kRowsTile;
+    }
+    __host__ __device__ static size_t bytes(int T, int m) { return 4 * (floats(T, m) + T + 4 * kRowsTile); }
+};
+
+// o[token][f0 + f] = w . x for 16 NF features of a warp (f0 and on, 128 apart) and its tokens, in groups of
+// 8: nk rows of k, then nq of q, o's rows on from each other's. W's fragments stay in registers; the next
+// group's rows are asked for one group ahead.
+template <int D, bool BF16, int NF>
+__device__ __forceinline__ void rows_logits(const void *Wv, int f0, const void *k, int nk, float *ok, const void *q, int nq,
+                                            float *oq, int ld, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    constexpr int NJ = BF16 ? D / 32 : D / 16;
+    constexpr size_t es = BF16 ? 2 : 4;
+    uint4 w[NF][2][NJ];
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                w[f][h][j] = __ldg((const uint4 *)((const char *)Wv + ((size_t)(f0 + 128 * f + g + 8 * h) * D + (16 / es) * t) * es + 64 * j));
+    const int gk = (nk + 7) / 8, gq = (nq + 7) / 8;
+    uint4 next[NJ];
+    auto ask = [&](int i) {
+        const bool key = i < gk;
+        const int row = 8 * (key ? i : i - gk) + g;
+        const bool in = i < gk + gq && row < (key ? nk : nq);
+        const char *x = (const char *)(key ? k : q) + ((size_t)row * D + (16 / es) * t) * es;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) next[j] = in ? __ldg((const uint4 *)(x + 64 * j)) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    ask(0);
+    for (int i = 0; i < gk + gq; ++i) {
+        const bool key = i < gk;
+        const int t0 = 8 * (key ? i : i - gk), n = key ? nk : nq;
+        float *o = key ? ok : oq;
+        uint4 xb[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) xb[j] = next[j];
+        ask(i + 1);
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+            float d[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f}, d2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const uint4 wa = w[f][0][j], wb = w[f][1][j];
+                if constexpr (BF16) {
+                    mma_bf16_16x8x16(d, wa.x, wb.x, wa.y, wb.y, xb[j].x, xb[j].y);
+                    mma_bf16_16x8x16(d1, wa.z, wb.z, wa.w, wb.w, xb[j].z, xb[j].w);
+                } else {
+                    const uint32_t xs[4] = {xb[j].x, xb[j].y, xb[j].z, xb[j].w}, a0[4] = {wa.x, wa.y, wa.z, wa.w},
+                                   a1[4] = {wb.x, wb.y, wb.z, wb.w};
+                    uint32_t bh[4], bl[4], ah[2][4], al[2][4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        tf32_split(__uint_as_float(xs[e]), bh[e], bl[e]);
+                        tf32_split(__uint_as_float(a0[e]), ah[0][e], al[0][e]);
+                        tf32_split(__uint_as_float(a1[e]), ah[1][e], al[1][e]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        mma_tf32_16x8x8(d1, al[0][e], al[1][e], al[0][e + 1], al[1][e + 1], bh[e], bh[e + 1]);
+                        mma_tf32_16x8x8(d2, ah[0][e], ah[1][e], ah[0][e + 1], ah[1][e + 1], bl[e], bl[e + 1]);
+                        mma_tf32_16x8x8(d, ah[0][e], ah[1][e], ah[0][e + 1], ah[1][e + 1], bh[e], bh[e + 1]);
+                    }
+                }
+            }
+            float *at = o + (size_t)(t0 + 2 * t) * ld + f0 + 128 * f + g;
+            if (t0 + 2 * t < n) {
+                at[0] = d[0] + (d1[0] + d2[0]);
+                at[8] = d[2] + (d1[2] + d2[2]);
+            }
+            if (t0 + 2 * t + 1 < n) {
+                at[ld] = d[1] + (d1[1] + d2[1]);
+                at[ld + 8] = d[3] + (d1[3] + d2[3]);
+            }
+        }
+    }
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kRowsThreads, 1) k_decode_tree_rows(TreeParams p) {
+    extern __shared__ __align__(16) float sm[];
+    const int bh = blockIdx.x, b = bh / p.H, m = p.m, T = p.T, i0 = blockIdx.y * kRowsTile, c0 = blockIdx.z * kRowsCols;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    constexpr int nw = kRowsThreads / 32;
+    const int n = tree_count(p.n_nodes, b, T);
+    if (i0 >= n) return;
+    const int rows = min(kRowsTile, n - i0), nk = i0 + rows;  // ancestors come first: keys 0 .. nk-1
+    const int ld = m + 16, ldy = RowsSmem::ldy(T);
+    float *sA = sm, *sB = sA + (size_t)T * ld, *sBs = sB + kRowsTile * ld, *sV = sBs + kRowsTile * ld;
+    float *sY = sV + (size_t)T * kRowsCols, *sEr = sY + (size_t)kRowsTile * ldy, *sDs = sEr + m, *sZ = sDs + m, *sE = sZ + m;
+    float *sTop = sE + T, *sC = sTop + 8;  // warps' maxima; [16][4] y, state's scale, denominator
+    int *sPar = (int *)(sC + 4 * kRowsTile);
+    uint32_t *sVis = (uint32_t *)(sPar + T);  // [16][4]
+    const size_t es = BF16 ? 2 : 4, row0 = (size_t)bh * T * D;
+
+    // this warp's 8 state columns, as fragments
+    const float *S = p.state + (size_t)bh * ((size_t)D * m + 2 * m);
+    const float *col = S + (size_t)(c0 + 8 * warp + g) * m + 4 * t;
+    float4 sf[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        if (16 * j < m) sf[j] = __ldg((const float4 *)(col + 16 * j));
+    float zr = 0.f, Dr = 0.f;
+    if (tid < m) {
+        zr = S[(size_t)D * m + tid];
+        Dr = S[(size_t)D * m + m + tid];
+    }
+    for (int i = tid; i < nk; i += kRowsThreads) sPar[i] = tree_parent(p.parents + (size_t)b * T, i);
+    for (int i = tid; i < nk * kRowsCols; i += kRowsThreads)
+        sV[i] = ld_elem(p.v, BF16, row0 + (size_t)(i / kRowsCols) * D + c0 + i % kRowsCols);
+    {
+        const void *k = (const char *)p.k + row0 * es, *q = (const char *)p.q + (row0 + (size_t)i0 * D) * es;
+        const int f = 16 * warp;
+        if (f + 128 < m && (BF16 || D == 64)) {
+            rows_logits<D, BF16, (BF16 || D == 64) ? 2 : 1>(p.W, f, k, nk, sA, q, rows, sB, ld, lane);
+        } else {
+            for (int f1 = f; f1 < m; f1 += 128) rows_logits<D, BF16, 1>(p.W, f1, k, nk, sA, q, rows, sB, ld, lane);
+        }
+    }
+    for (int j = warp; j < nk; j += nw) {
+        float x = 0.f;
+#pragma unroll
+        for (int c = lane; c < D; c += 32) {
+            const float k = ld_elem(p.k, BF16, row0 + (size_t)j * D + c);
+            x = fmaf(k, k, x);
+        }
+        x = warp_sum(x);
+        if (lane == 0) sE[j] = -0.5f * x;
+    }
+    __syncthreads();
+    // a: a feature a thread
+    float ds = -INFINITY;
+    if (tid < m) {
+        float E = -INFINITY;
+        for (int j = 0; j < nk; ++j) {
+            const float x = sA[(size_t)j * ld + tid];
+            if (fabsf(x) < INFINITY) E = fmaxf(E, x);
+        }
+        if (E == -INFINITY) E = 0.f;  // no finite logit
+#pragma unroll 4
+        for (int j = 0; j < nk; ++j) sA[(size_t)j * ld + tid] = expf(sA[(size_t)j * ld + tid] - E);
+        if (zr != 0.f) ds = Dr - E;
+        sEr[tid] = E;
+        sDs[tid] = ds;
+        sZ[tid] = zr;
+    }
+    if (tid >= kRowsThreads - 32 && lane < rows) {  // the rows' visible sets
+        uint32_t x[4] = {0u, 0u, 0u, 0u};
+        for (int j = i0 + lane; j >= 0; j = sPar[j]) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) x[w] |= (j >> 5) == w ? 1u << (j & 31) : 0u;
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) sVis[4 * lane + w] = x[w];
+    }
+    const float dw = warp_max(ds);
+    if (lane == 0) sTop[warp] = dw;
+    __syncthreads();
+    float eS = sTop[0];
+#pragma unroll
+    for (int w = 1; w < nw; ++w) eS = fmaxf(eS, sTop[w]);
+    // b and b s: a warp a row
+    for (int i = warp; i < kRowsTile; i += nw) {
+        float u[8], f = -INFINITY, y = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = lane + 32 * k;
+            u[k] = r < m && i < rows ? sB[i * ld + r] + sEr[r] : -INFINITY;
+            f = fmaxf(f, u[k]);
+        }
+        f = warp_max(f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = lane + 32 * k;
+            if (r < m) {
+                const float x = i < rows ? expf(u[k] - f) : 0.f;
+                const float s = sZ[r] != 0.f ? expf(sDs[r] - eS) : 0.f;
+                sB[i * ld + r] = x;
+                sBs[i * ld + r] = x * s;
+                y = fmaf(x * s, sZ[r], y);
+            }
+        }
+        y = warp_sum(y);
+        if (lane == 0) sC[4 * i] = y;
+    }
+    __syncthreads();
+    // products over the features, 8 columns a warp: the state's, then the keys'
+    for (int nt = warp; nt < nw + (nk + 7) / 8; nt += nw) {
+        const bool state = nt < nw;
+        const int j0 = 8 * (nt - nw);
+        const float *A = (state ? sBs : sB) + g * ld + 4 * t, *B = sA + (size_t)(j0 + g) * ld + 4 * t;
+        const bool in = !state && j0 + g < nk;
+        float d[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f}, d2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            if (16 * j < m) {
+                const float4 a0 = *(const float4 *)(A + 16 * j), a1 = *(const float4 *)(A + 8 * ld + 16 * j);
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (state)
+                    x = sf[j];
+                else if (in)
+                    x = *(const float4 *)(B + 16 * j);
+                const float xs[4] = {x.x, x.y, x.z, x.w}, as[2][4] = {{a0.x, a0.y, a0.z, a0.w}, {a1.x, a1.y, a1.z, a1.w}};
+                uint32_t bh[4], bl[4], ah[2][4], al[2][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    tf32_split(xs[i], bh[i], bl[i]);
+                    tf32_split(as[0][i], ah[0][i], al[0][i]);
+                    tf32_split(as[1][i], ah[1][i], al[1][i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    mma_tf32_16x8x8(d1, al[0][i], al[1][i], al[0][i + 1], al[1][i + 1], bh[i], bh[i + 1]);
+                    mma_tf32_16x8x8(d2, ah[0][i], ah[1][i], ah[0][i + 1], ah[1][i + 1], bl[i], bl[i + 1]);
+                    mma_tf32_16x8x8(d, ah[0][i], ah[1][i], ah[0][i + 1], ah[1][i + 1], bh[i], bh[i + 1]);
+                }
+            }
+        }
+        float *y = sY + (size_t)g * ldy + 8 * nt + 2 * t;
+        y[0] = d[0] + (d1[0] + d2[0]);
+        y[1] = d[1] + (d1[1] + d2[1]);
+        y[8 * ldy] = d[2] + (d1[2] + d2[2]);
+        y[8 * ldy + 1] = d[3] + (d1[3] + d2[3]);
+    }
+    __syncthreads();
+    // per row: the visible nodes' scales, the weights and the denominator
+    for (int i = warp; i < rows; i += nw) {
+        float M = eS, w[4], den = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            w[k] = (sVis[4 * i + k] >> lane) & 1u ? sE[32 * k + lane] : -INFINITY;
+            M = fmaxf(M, w[k]);
+        }
+        M = warp_max(M);
+        const float cS = eS == -INFINITY ? 0.f : expf(eS - M);
+        float *y = sY + (size_t)i * ldy + kRowsCols;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if ((sVis[4 * i + k] >> lane) & 1u) {
+                const float x = expf(w[k] - M) * y[32 * k + lane];
+                y[32 * k + lane] = x;
+                den += x;
+            }
+        den = warp_sum(den);
+        if (lane == 0) {
+            sC[4 * i + 1] = cS;
+            sC[4 * i + 2] = cS == 0.f ? den : fmaf(cS, sC[4 * i], den);
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < rows * kRowsCols; i += kRowsThreads) {
+        const int r = i / kRowsCols, c = i % kRowsCols;
+        const float *y = sY + (size_t)r * ldy, cS = sC[4 * r + 1], den = sC[4 * r + 2];
+        if (!(den >= kTreeDenMin)) continue;
+        float num = cS == 0.f ? 0.f : cS * y[c];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            for (uint32_t x = sVis[4 * r + k]; x != 0; x &= x - 1) {
+                const int j = 32 * k + __ffs(x) - 1;
+                num = fmaf(y[kRowsCols + j], sV[j * kRowsCols + c], num);
+            }
+        p.out[row0 + (size_t)(i0 + r) * D + c0 + c] = num / den;
+    }
+    if (c0 == 0)
+        for (int i = warp; i < rows; i += nw)
+            if (!(sC[4 * i + 2] >= kTreeDenMin)) tree_row_exact<D>(p, bh, i0 + i, sPar);
+}
+
+template <int D, bool BF16>
 static cudaError_t launch_tree_rows(const TreeParams &p, cudaStream_t st) {
-    const size_t sm = TreeSmem<D>::bytes(TQ, p.T, p.m);
-    cudaError_t e = cudaFuncSetAttribute(k_decode_tree_rows<D, TQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+    const size_t sm = RowsSmem::bytes(p.T, p.m);
+    const cudaError_t e = cudaFuncSetAttribute(k_decode_tree_rows<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
     if (e != cudaSuccess) return e;
-    k_decode_tree_rows<D, TQ><<<dim3(p.B * p.H, (p.T + TQ - 1) / TQ), kTreeThreads, sm, st>>>(p);
+    const dim3 grid(p.B * p.H, (p.T + kRowsTile - 1) / kRowsTile, D / kRowsCols);
+    k_decode_tree_rows<D, BF16><<<grid, kRowsThreads, sm, st>>>(p);
     return cudaGetLastError();
 }
 
@@ -676,8 +785,7 @@ template <int D>
 static cudaError_t launch_decode_tree_d(const TreeParams &p, cudaStream_t st) {
     if (p.T == 1) return launch_tree_few<D, 1>(p, st);
     if (p.T <= 4) return launch_tree_few<D, 4>(p, st);
-    if (p.T <= 8) return launch_tree_few<D, 8>(p, st);
-    return launch_tree_rows<D, 16>(p, st);
+    return p.bf16 ? launch_tree_rows<D, true>(p, st) : launch_tree_rows<D, false>(p, st);
 }
 
 cudaError_t launch_decode_tree(const TreeParams &p, int d, cudaStream_t st) {
