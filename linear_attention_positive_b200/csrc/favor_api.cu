@@ -1143,10 +1143,10 @@ struct ExtendPlan {
 ExtendPlan extend_plan(const favor_shape *s, int n_tok, bool indexed) {
     const long long BH = (long long)s->B * s->H;
     if (s->dtype == FAVOR_BF16 && !indexed && n_tok >= kExtTcMin) {
-        const long long nt = (n_tok - 1) / kTile + 1, rows = BH * ((s->m + 127) / 128);
+        const long long nt = (n_tok - 1) / kExtTile + 1, rows = BH * ((s->m + 127) / 128);
         const long long runs = std::max<long long>(1, std::min(nt, 2ll * num_sms() / rows));
         const long long per = (nt + runs - 1) / runs;
-        return {true, (int)((nt + per - 1) / per), (int)(per * kTile)};
+        return {true, (int)((nt + per - 1) / per), (int)(per * kExtTile)};
     }
     if (n_tok <= kExtWhole) return {false, 1, n_tok};
     const long long ctas = 4ll * num_sms();
@@ -1182,7 +1182,7 @@ extern "C" favor_status favor_decode_tree(const favor_shape *s, const void *q, c
 extern "C" size_t favor_decode_extend_workspace_size(const favor_shape *s, int n_index) {
     if (!shape_ok(s) || n_index < 0 || !decode_supported(s)) return 0;
     const ExtendPlan pl = extend_plan(s, n_index > 0 ? n_index : s->L, n_index > 0);
-    if (pl.n_split == 1) return 256;
+    if (pl.n_split == 1 && !(pl.tc && s->d == 128)) return 256;  // (on tiles, d = 128 sums in a partial state)
     return align256((size_t)s->B * s->H * pl.n_split * ((size_t)s->d * s->m + 2 * s->m) * 4);
 }
 
@@ -1204,8 +1204,8 @@ extern "C" favor_status favor_decode_extend(const favor_shape *s, const void *k,
                    (float *)workspace, pl.n_split, pl.tok_per_split};
     if (!pl.tc) return cuda_status(launch_decode_extend(p, s->d, (cudaStream_t)stream));
     CUtensorMap mK, mV, mW;
-    if (!make_token_map(&mK, k, s->B * s->H, s->L, s->d) || !make_token_map(&mV, v, s->B * s->H, s->L, s->d) ||
-        !make_w_map(&mW, W, s->m, s->d, 128))
+    if (!make_token_map(&mK, k, s->B * s->H, s->L, s->d, kExtTile) ||
+        !make_token_map(&mV, v, s->B * s->H, s->L, s->d, kExtTile) || !make_w_map(&mW, W, s->m, s->d, 128))
         return FAVOR_ERR_CUDA;
     return cuda_status(launch_decode_extend_tc(mK, mV, mW, p, s->d, (cudaStream_t)stream));
 }

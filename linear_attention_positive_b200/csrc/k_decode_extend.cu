@@ -62,10 +62,7 @@ __global__ void __launch_bounds__(256) k_decode_extend_rows(ExtendParams p) {
     float *S = whole ? p.state + (size_t)bh * len : p.part + ((size_t)bh * p.n_split + split) * len;
     float *z = S + (size_t)D * m, *Dl = z + m;
     const int t0 = split * p.tok_per_split, t1 = min(n, t0 + p.tok_per_split);
-    if (t0 >= t1) {  // an empty run: nothing but its mark is read back
-        z[r] = 0.f;
-        return;
-    }
+    if (t0 >= t1) return;  // an empty run
     float s[D], zr = 0.f, Dr = -INFINITY;
     if (split == 0) {  // the first run starts from the carried state
         const float *S0 = p.state + (size_t)bh * len;
@@ -129,10 +126,7 @@ __global__ void __launch_bounds__(256) k_decode_extend_rows(ExtendParams p) {
             }
         }
     }
-    if (zr == 0.f) {  // no token entered this feature
-        if (!whole) z[r] = 0.f;
-        return;
-    }
+    if (zr == 0.f && whole) return;  // no token entered this feature
 #pragma unroll
     for (int c = 0; c < D; ++c) S[(size_t)c * m + r] = s[c];
     z[r] = zr;
@@ -264,29 +258,51 @@ static cudaError_t launch_extend_path(const ExtendParams &p, cudaStream_t st) {
 }
 
 // Adds the partial states of a head's runs (the first holds the carried state) into the state: one
-// thread per feature, kCombCols value columns per CTA; the CTA of the first columns writes z' and D.
-constexpr int kCombCols = 8;
+// thread per feature, kCombCols value columns per CTA; the CTA of the first columns writes z' and D. One
+// pass with a running maximum, kCombRuns runs' loads in flight at a time (left to the compiler they were
+// taken one after another: 2 us a run).
+constexpr int kCombCols = 4, kCombRuns = 8;
 
 __global__ void __launch_bounds__(256) k_extend_combine(ExtendParams p, int d) {
     const int bh = blockIdx.y, r = threadIdx.x, m = p.m, c0 = blockIdx.x * kCombCols;
     const size_t len = (size_t)d * m + 2 * m;
-    if (extend_count(p, bh / p.H) == 0) return;
+    const int n = extend_count(p, bh / p.H);
+    if (n == 0) return;
+    const int runs = (n - 1) / p.tok_per_split + 1;  // the others are empty, and not written
     const float *part = p.part + (size_t)bh * p.n_split * len + r;
     float *S = p.state + (size_t)bh * len + r;
     const size_t oz = (size_t)d * m, oD = oz + m;
-    float D = -INFINITY;
-    for (int s = 0; s < p.n_split; ++s)
-        if (part[s * len + oz] != 0.f) D = fmaxf(D, part[s * len + oD]);
-    float acc[kCombCols], z = 0.f;
+    float D = -INFINITY, acc[kCombCols], z = 0.f;
 #pragma unroll
     for (int c = 0; c < kCombCols; ++c) acc[c] = 0.f;
-    for (int s = 0; s < p.n_split; ++s) {
-        const float zs = part[s * len + oz];
-        if (zs == 0.f) continue;
-        const float w = expf(part[s * len + oD] - D);
-        z = fmaf(w, zs, z);
+    for (int s0 = 0; s0 < runs; s0 += kCombRuns) {
+        float zs[kCombRuns], Ds[kCombRuns], x[kCombRuns][kCombCols];
 #pragma unroll
-        for (int c = 0; c < kCombCols; ++c) acc[c] = fmaf(w, part[s * len + (size_t)(c0 + c) * m], acc[c]);
+        for (int i = 0; i < kCombRuns; ++i) {
+            const float *at = part + min(s0 + i, runs - 1) * len;
+            zs[i] = __ldcg(at + oz);
+            Ds[i] = __ldcg(at + oD);
+#pragma unroll
+            for (int c = 0; c < kCombCols; ++c) x[i][c] = __ldcg(at + (size_t)(c0 + c) * m);
+        }
+        float Dn = D;
+#pragma unroll
+        for (int i = 0; i < kCombRuns; ++i) {
+            if (s0 + i >= runs) zs[i] = 0.f;
+            Dn = zs[i] != 0.f ? fmaxf(Dn, Ds[i]) : Dn;
+        }
+        const float keep = z != 0.f ? expf(D - Dn) : 0.f;
+        D = Dn;
+        z *= keep;
+#pragma unroll
+        for (int c = 0; c < kCombCols; ++c) acc[c] *= keep;
+#pragma unroll
+        for (int i = 0; i < kCombRuns; ++i) {
+            const float w = zs[i] != 0.f ? expf(Ds[i] - Dn) : 0.f;
+            z = fmaf(w, zs[i], z);
+#pragma unroll
+            for (int c = 0; c < kCombCols; ++c) acc[c] = s0 + i < runs ? fmaf(w, x[i][c], acc[c]) : acc[c];
+        }
     }
     if (z == 0.f) return;
 #pragma unroll

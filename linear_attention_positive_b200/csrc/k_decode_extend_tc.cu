@@ -1,40 +1,47 @@
 // favor_decode_extend on tensor cores: bf16 tokens in order (no index), long enough to fill tiles.
 //
-// One CTA per (run of 128-token tiles, half of 128 features, head), two CTAs an SM, so that one CTA's
-// MMAs and loads run under the other's exponentials. Per tile:
-//   P^T = W_h K^T - |k|^2/2    tcgen05 (M = 128 features, N = 128 tokens), bf16 operands (exact
+// One CTA per (run of 64-token tiles, half of 128 features, head), two CTAs an SM. Per tile:
+//   P^T = W_h K^T - |k|^2/2    tcgen05 (M = 128 features, N = 64 tokens), bf16 operands (exact
 //                              products); the norm enters as a K = 16 step of three bf16 parts per key
 //                              against ones columns of W (-inf for a key past the sequence's count);
 //   phi' = 2^(P log2e - D_r)   one thread per feature; D_r, an integer, is set so that the first
 //                              tile's largest exponent lands in (7, 8] and raised whenever a tile's
 //                              passes 15 (fp16 holds 2^t below 2^16);
-//   acc = phi'^T V'            tcgen05 (M = 128, N = d, K = 128), fp16 operands: phi' = hi + lo, two fp16
-//                              values (22 bits), A from TMEM where they replace P chunk by chunk;
-//                              V' = V 2^-b, exact in fp16 but for entries 2^-22 of the tile's largest;
-//   S_r += 2^b acc             in fp32 registers, tile by tile: the tensor core's own accumulation
-//                              truncates, and over a long run that bias would reach 1e-5.
+//   acc += phi'^T V'           tcgen05 (M = 128, N = d, K = 64), fp16 operands: phi' = hi + lo, two fp16
+//                              values (22 bits), A from TMEM where they replace P; V' = V 2^-b, exact in
+//                              fp16 but for entries 2^-20 of the tile's largest and below (off by 2^-21 of it);
+//   S_r <- 2^(..) S_r + 2^b acc  in fp32, every kExtFlush tiles and before a tile that changes D_r or b:
+//                              the tensor core's own accumulation truncates; over 512 tokens that bias
+//                              stays near 2e-6, over a long run it would reach 1e-5.
 // A single fp16 phi' would cost 1e-4 relative in S (the roundings do not average out against values of
 // both signs); with hi + lo the state has fp32 precision and the MMA work is 1.5 times the least.
 //
+// P is double-buffered: while the exponent warps work on one tile, the MMAs of the tile before (S) and
+// the one after (P) run, so that the exponent warps do not wait for a round trip of the tensor core
+// (with one buffer of 128 tokens they did: 283 us for 65536 tokens in 16 heads at d = 64, m = 256).
 // Bound: 2^t on the MUFU (16 a cycle and SM): B H L m of them; next the tensor work, 6 L m d a head.
 //
-// Warps 0-3: exponentials, z_r, and value columns 64.. of S for d = 128. Warps 4-7: |k|^2 and norms'
-// extension, V -> fp16, value columns 0..63 of S. Warp 8: TMA and MMA issue.
+// Warps 0-3: exponentials and z_r. Warps 4-7: |k|^2 and the norms' extension, V -> fp16, S. Warp 8: TMA
+// and MMA issue. Every barrier that a group waits on is at most one phase ahead of it, but d_full, which
+// has four slots: the exponent warps may be two tiles ahead of warps 4-7 there.
 
 #include "common.cuh"
 
 namespace favor {
 
+constexpr int kExtTile = 64;
+constexpr int kExtFlush = 8;
+
 template <int D_>
 struct ExtTc {
     static constexpr int D = D_, NB = D / 64;
-    static constexpr int NS = D == 64 ? 2 : 1;  // K and V stages each (227 KB for two CTAs)
-    static constexpr uint32_t BLK = kTile * 128, KT = NB * BLK;
+    static constexpr int NS = D == 64 ? 4 : 2;  // K and V stages each (227 KB for two CTAs)
+    static constexpr uint32_t WBLK = 128 * 128, WT = NB * WBLK, BLK = kExtTile * 128, KT = NB * BLK, KX = kExtTile * 32;
     static constexpr int THREADS = 288;
-    static constexpr uint32_t T_P = 0, T_ACC = 128;  // TMEM columns
-    static constexpr size_t OFF_K = KT, OFF_V = OFF_K + NS * KT, OFF_KX = OFF_V + NS * KT, OFF_WX = OFF_KX + NS * 4096,
-                            OFF_D = OFF_WX + 4096, OFF_F = OFF_D + 2 * 128 * 4, OFF_MISC = OFF_F + 128 * 8,
-                            OFF_BAR = OFF_MISC + 64, BYTES = OFF_BAR + 256 + 1024;
+    static constexpr uint32_t T_P = 0, T_ACC = 128;  // TMEM columns: two tiles of P, the accumulator
+    static constexpr size_t OFF_K = WT, OFF_V = OFF_K + NS * KT, OFF_KX = OFF_V + NS * KT, OFF_WX = OFF_KX + NS * KX,
+                            OFF_D = OFF_WX + 4096, OFF_F = OFF_D + 4 * 128 * 4, OFF_MISC = OFF_F + 128 * 8,
+                            OFF_BAR = OFF_MISC + 128, BYTES = OFF_BAR + 256 + 1024;
 };
 
 template <int D>
@@ -46,14 +53,15 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sW = smem, *sK = smem + C::OFF_K, *sV = smem + C::OFF_V, *sKx = smem + C::OFF_KX, *sWx = smem + C::OFF_WX;
-    float *sD = (float *)(smem + C::OFF_D);      // [2 tile parities][128]: D_r of the tile
-    float2 *sF = (float2 *)(smem + C::OFF_F);    // [128]: final factors of the run's and the old S'
-    int *sShift = (int *)(smem + C::OFF_MISC);   // [4]: b of tile g
-    uint32_t *sRed = (uint32_t *)(sShift + 4);   // [2][4]
+    float *sD = (float *)(smem + C::OFF_D);       // [tile % 4][128]: D_r
+    float2 *sF = (float2 *)(smem + C::OFF_F);     // [128]: final factors of the run's and the old S'
+    int *sRaise = (int *)(smem + C::OFF_MISC);    // [tile % 4][warp]: some D_r of this warp's changes here
+    int *sScale = sRaise + 16;                    // [tile % 4]: b changes here
+    uint32_t *sRed = (uint32_t *)(sScale + 4);    // [2][4]
     uint64_t *bars = (uint64_t *)(smem + C::OFF_BAR);
-    uint64_t *w_full = bars, *k_full = bars + 1, *v_full = k_full + NS, *k_conv = v_full + NS, *v_conv = k_conv + NS;
-    uint64_t *p_full = v_conv + NS, *phi_full = p_full + 1, *s_full = phi_full + 4, *acc_free = s_full + 1;
-    uint64_t *d_full = acc_free + 1, *v_max = d_full + 2, *drain = v_max + 1;
+    uint64_t *k_full = bars, *v_full = k_full + NS, *k_conv = v_full + NS, *v_conv = k_conv + NS;
+    uint64_t *p_full = v_conv + NS, *phi_full = p_full + 2, *s_done = phi_full + 2, *d_full = s_done + 2;
+    uint64_t *w_full = d_full + 4, *acc_full = w_full + 1, *acc_free = w_full + 2, *v_max = w_full + 3, *drain = w_full + 4;
     uint32_t *tmem_slot = (uint32_t *)(drain + 1);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
 
@@ -61,32 +69,30 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
     const int split = blockIdx.x, half = blockIdx.y, bh = blockIdx.z;
     const int count = extend_count(p, bh / p.H);
     if (count == 0) return;  // the state stays as it is
-    const int t0 = split * p.tok_per_split / kTile;  // tok_per_split is a multiple of the tile
-    const int t1 = min((count - 1) / kTile + 1, t0 + p.tok_per_split / kTile);
+    const int t0 = split * (p.tok_per_split / kExtTile);  // tok_per_split is a multiple of the tile
+    const int t1 = min((count - 1) / kExtTile + 1, t0 + p.tok_per_split / kExtTile);
     const int n = t1 - t0, m = p.m;
     const size_t len = (size_t)D * m + 2 * m;
-    const bool whole = p.n_split == 1;
+    const bool whole = p.n_split == 1 && D == 64;
     float *dst = whole ? p.state + (size_t)bh * len : p.part + ((size_t)bh * p.n_split + split) * len;
-    if (n <= 0) {  // an empty run: nothing but its mark is read back
-        const int r = half * 128 + threadIdx.x;
-        if (threadIdx.x < 128 && r < m) dst[(size_t)D * m + r] = 0.f;
-        return;
-    }
+    if (n <= 0) return;  // an empty run
 
     if (threadIdx.x == 0) {
-        mbar_init(w_full, 1);
         for (int s = 0; s < NS; ++s) {
             mbar_init(&k_full[s], 1);
             mbar_init(&v_full[s], 1);
             mbar_init(&k_conv[s], 128);
             mbar_init(&v_conv[s], 128);
         }
-        mbar_init(p_full, 1);
-        for (int c = 0; c < 4; ++c) mbar_init(&phi_full[c], 128);
-        mbar_init(s_full, 1);
-        mbar_init(acc_free, D == 64 ? 128 : 256);
-        mbar_init(&d_full[0], 128);
-        mbar_init(&d_full[1], 128);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&p_full[s], 1);
+            mbar_init(&phi_full[s], 128);
+            mbar_init(&s_done[s], 1);
+        }
+        for (int s = 0; s < 4; ++s) mbar_init(&d_full[s], 128);
+        mbar_init(w_full, 1);
+        mbar_init(acc_full, 1);
+        mbar_init(acc_free, 128);
         mbar_init(v_max, 128);
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -102,71 +108,87 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
         *(uint4 *)(sWx + (r >> 3) * 256 + kc * 128 + (r & 7) * 16) =
             kc == 0 ? make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
     }
-    for (int i = threadIdx.x; i < NS * 128; i += C::THREADS)
-        *(uint4 *)(sKx + (i >> 7) * 4096 + ((i & 127) >> 3) * 256 + 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = threadIdx.x; i < NS * kExtTile; i += C::THREADS)
+        *(uint4 *)(sKx + (i / kExtTile) * C::KX + ((i % kExtTile) >> 3) * 256 + 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
     fence_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // whether S takes the accumulator before tile g adds to it (read after tile g's d_full or phi_full);
+    // scale: b changes with tile g
+    auto flush_before = [&](int g, bool scale) {
+        const int *r = sRaise + 4 * (g & 3);
+        return g > 0 && ((g % kExtFlush) == 0 || scale || (r[0] | r[1] | r[2] | r[3]) != 0);
+    };
 
     if (warp == 8) {
         auto load = [&](const CUtensorMap *map, uint8_t *buf, uint64_t *bar, int g) {
             if (elect_one()) {
                 mbar_arrive_expect_tx(&bar[g % NS], C::KT);
                 for (int nb = 0; nb < NB; ++nb)
-                    tma_load_3d(buf + (size_t)(g % NS) * C::KT + nb * C::BLK, map, &bar[g % NS], 64 * nb, (t0 + g) * kTile, bh);
+                    tma_load_3d(buf + (size_t)(g % NS) * C::KT + nb * C::BLK, map, &bar[g % NS], 64 * nb, (t0 + g) * kExtTile, bh);
             }
             __syncwarp();
         };
+        int nk = 0, nv = 0;  // K and V tiles asked for
+        load(&mapK, sK, k_full, nk++);
         if (elect_one()) {
-            mbar_arrive_expect_tx(w_full, C::KT);
-            for (int nb = 0; nb < NB; ++nb) tma_load_2d(sW + nb * C::BLK, &mapW, w_full, 64 * nb, half * 128);
+            mbar_arrive_expect_tx(w_full, C::WT);
+            for (int nb = 0; nb < NB; ++nb) tma_load_2d(sW + nb * C::WBLK, &mapW, w_full, 64 * nb, half * 128);
         }
         __syncwarp();
-        int nk = 0, nv = 0;  // K and V tiles asked for
         for (; nk < min(NS, n); ++nk) load(&mapK, sK, k_full, nk);
         for (; nv < min(NS, n); ++nv) load(&mapV, sV, v_full, nv);
-        const uint32_t idesc_p = make_idesc(128, 128, kFmtBF16, 0, 0), idesc_s = make_idesc(128, D, kFmtF16, 0, 1);
+        const uint32_t idesc_p = make_idesc(128, kExtTile, kFmtBF16, 0, 0), idesc_s = make_idesc(128, D, kFmtF16, 0, 1);
         const uint64_t dW = make_sdesc(smem_u32(sW), 16, 1024), dK = make_sdesc(smem_u32(sK), 16, 1024);
         const uint64_t dV = make_sdesc(smem_u32(sV), C::BLK, 1024);
         const uint64_t dWx = make_sdesc_interleaved(smem_u32(sWx), 128, 256);
         const uint64_t dKx = make_sdesc_interleaved(smem_u32(sKx), 128, 256);
         bool ok = mbar_wait_all(w_full, 0, abort_flag);
-        for (int g = 0; ok && g < n; ++g) {
-            const int s = g % NS;
-            const uint32_t ph = (g / NS) & 1;
-            // P's columns still hold phi'(g - 1) until the state MMA of tile g - 1 has read them
-            if (g > 0) ok = mbar_wait_all(s_full, (g - 1) & 1, abort_flag);
-            if (!ok) break;
-            if (g > 0 && nv < n) load(&mapV, sV, v_full, nv++);
-            ok = mbar_wait_all(&k_full[s], ph, abort_flag) && mbar_wait_all(&k_conv[s], ph, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            for (int nb = 0; nb < NB; ++nb)
-                mma_ss_x4_w(tmem + C::T_P, dW + nb * (C::BLK / 16), dK + s * (C::KT / 16) + nb * (C::BLK / 16), idesc_p,
-                            nb > 0, 2, 2);
-            mma_f16_ss_w(tmem + C::T_P, dWx, dKx + s * (4096 / 16), idesc_p, 1u);
-            mma_commit_w(p_full);
-            ok = mbar_wait_all(p_full, g & 1, abort_flag);
-            if (!ok) break;
-            if (nk < n) load(&mapK, sK, k_full, nk++);
-            ok = mbar_wait_all(&v_full[s], ph, abort_flag) && mbar_wait_all(&v_conv[s], ph, abort_flag);
-            if (ok && g > 0) ok = mbar_wait_all(acc_free, (g - 1) & 1, abort_flag);
-            const uint64_t dVs = dV + s * (C::KT / 16);
-            for (int c = 0; ok && c < 4; ++c) {
-                ok = mbar_wait_all(&phi_full[c], g & 1, abort_flag);
+        int flushes = 0;
+        for (int i = 0; ok && i <= n; ++i) {
+            if (i < n) {  // P of tile i, where phi' of tile i - 2 was
+                const int s = i % NS;
+                if (i >= 2) {
+                    if (!(ok = mbar_wait_all(&s_done[i & 1], ((i >> 1) - 1) & 1, abort_flag))) break;
+                    if (nv < n) load(&mapV, sV, v_full, nv++);
+                }
+                if (!(ok = mbar_wait_all(&k_conv[s], (i / NS) & 1, abort_flag))) break;
+                tc_fence_after();
+                const uint32_t P = tmem + C::T_P + kExtTile * (i & 1);
+                for (int nb = 0; nb < NB; ++nb)
+                    mma_ss_x4_w(P, dW + nb * (C::WBLK / 16), dK + s * (C::KT / 16) + nb * (C::BLK / 16), idesc_p, nb > 0, 2, 2);
+                mma_f16_ss_w(P, dWx, dKx + s * (C::KX / 16), idesc_p, 1u);
+                mma_commit_w(&p_full[i & 1]);
+            }
+            if (i >= 1) {  // S of tile i - 1
+                const int j = i - 1;
+                if (nk < n) {  // its keys are done with
+                    if (!(ok = mbar_wait_all(&p_full[j & 1], (j >> 1) & 1, abort_flag))) break;
+                    load(&mapK, sK, k_full, nk++);
+                }
+                ok = mbar_wait_all(&v_conv[j % NS], (j / NS) & 1, abort_flag) &&
+                     mbar_wait_all(&phi_full[j & 1], (j >> 1) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint64_t vd = dVs + (uint32_t)(32 * c + 16 * k) * 128 / 16;
-                    mma_f16_ts_w(tmem + C::T_ACC, tmem + C::T_P + 32 * c + 8 * k, vd, idesc_s, c + k > 0);
-                    mma_f16_ts_w(tmem + C::T_ACC, tmem + C::T_P + 32 * c + 16 + 8 * k, vd, idesc_s, 1u);
+                const bool fresh = flush_before(j, sScale[j & 3] != 0);
+                if (fresh) {
+                    mma_commit_w(acc_full);
+                    if (!(ok = mbar_wait_all(acc_free, flushes++ & 1, abort_flag))) break;
+                    tc_fence_after();
                 }
+                const uint32_t phi = tmem + C::T_P + kExtTile * (j & 1);
+                const uint64_t v = dV + (j % NS) * (C::KT / 16);
+#pragma unroll
+                for (int k = 0; k < kExtTile / 16; ++k) {
+                    mma_f16_ts_w(tmem + C::T_ACC, phi + 16 * k, v + k * (16 * 128 / 16), idesc_s, !(j == 0 || fresh) || k > 0);
+                    mma_f16_ts_w(tmem + C::T_ACC, phi + 16 * k + 8, v + k * (16 * 128 / 16), idesc_s, 1u);
+                }
+                mma_commit_w(&s_done[j & 1]);
             }
-            if (ok) mma_commit_w(s_full);
         }
+        if (ok) mma_commit_w(acc_full);
         // nothing of this CTA is in flight when it frees its memory
         mma_commit_w(drain);
         volatile int no_abort = 0;
@@ -178,115 +200,61 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
         const int row = (warp & 3) * 32 + lane, r = half * 128 + row;
         const uint32_t tL = tmem + (((uint32_t)(warp & 3) * 32u) << 16);
         const float *old = p.state + (size_t)bh * len;
-        constexpr int SC = 64;  // value columns of S a thread keeps
-        float S[SC];
-        float Dreg = 0.f;  // the units of S: 2^D
-        // S <- S 2^(Dreg - D(g)) + 2^b acc, for columns c0 .. c0 + 63
-        auto flush = [&](int g, int c0) {
-            const float Dg = sD[(g & 1) * 128 + row];
-            const float keep = exp2f(fminf(Dreg - Dg, 0.f));
-            Dreg = Dg;
-            const float up = __uint_as_float((uint32_t)(127 + sShift[g & 3]) << 23);
-            float v[16];
-#pragma unroll
-            for (int q = 0; q < SC; q += 16) {
-                tmem_ld16(tL + C::T_ACC + c0 + q, v);
-#pragma unroll
-                for (int c = 0; c < 16; c += 2) {
-                    float a, b;
-                    ffma2(v[c], v[c + 1], up, up, 0.f, 0.f, a, b);
-                    ffma2(S[q + c], S[q + c + 1], keep, keep, a, b, S[q + c], S[q + c + 1]);
-                }
-            }
-            tc_fence_before();
-            mbar_arrive(acc_free);
-        };
-        // the run's S' columns c0 .. c0 + 63 in the state's units, joined with the carried ones
-        auto finish = [&](int c0) {
-            const float2 f = sF[row];
-            if (r >= m || (f.x == 0.f && f.y == 0.f)) return;
-#pragma unroll
-            for (int c = 0; c < SC; ++c) {
-                const size_t at = (size_t)(c0 + c) * m + r;
-                float x = S[c] * f.x;
-                if (f.y != 0.f) x = fmaf(old[at], f.y, x);
-                dst[at] = x;
-            }
-        };
         bool ok = true;
         if (warp < 4) {
             float Dr = 0.f, z = 0.f, umax = -INFINITY;
-            if (D == 128) {
-#pragma unroll
-                for (int c = 0; c < SC; ++c) S[c] = 0.f;
-            }
             for (int g = 0; ok && g < n; ++g) {
-                if (!(ok = mbar_wait_all(p_full, g & 1, abort_flag))) break;
+                if (!(ok = mbar_wait_all(&p_full[g & 1], (g >> 1) & 1, abort_flag))) break;
                 tc_fence_after();
+                const uint32_t P = tL + C::T_P + kExtTile * (g & 1);
                 float va[32], vb[32];
+                tmem_ld32_nowait(P, va);
+                tmem_ld32_nowait(P + 32, vb);
+                tmem_wait_ld32(va);
+                tmem_wait_ld32(vb);
                 // the tile's largest u, then D_r
-                tmem_ld32_nowait(tL + C::T_P, va);
-                tmem_wait_ld32(va);
-                tmem_ld32_nowait(tL + C::T_P + 32, vb);
-                float um = chunk_vmax(va);
-                tmem_wait_ld32(vb);
-                tmem_ld32_nowait(tL + C::T_P + 64, va);
-                um = fmaxf(um, chunk_vmax(vb));
-                tmem_wait_ld32(va);
-                tmem_ld32_nowait(tL + C::T_P + 96, vb);
-                um = fmaxf(um, chunk_vmax(va));
-                tmem_wait_ld32(vb);
-                tmem_ld32_nowait(tL + C::T_P, va);
-                um = fmaxf(um, chunk_vmax(vb));
-                const float tm = um * kLog2e;
+                const float um = fmaxf(chunk_vmax(va), chunk_vmax(vb)), tm = um * kLog2e;
+                bool raise = false;
                 if (tm > -INFINITY && (umax == -INFINITY || tm - Dr > 15.f)) {
                     const float Dn = ceilf(tm) - 8.f;
                     z = z == 0.f ? 0.f : z * exp2f(Dr - Dn);
                     Dr = Dn;
+                    raise = true;
                 }
                 umax = fmaxf(umax, um);
-                sD[(g & 1) * 128 + row] = Dr;
-                mbar_arrive(&d_full[g & 1]);
-                auto chunk = [&](float(&v)[32], int c) {
-                    uint32_t hi[16], lo[16];
-                    float s0 = 0.f, s1 = 0.f;
+                sD[(g & 3) * 128 + row] = Dr;
+                raise = __any_sync(0xffffffffu, raise);
+                if (lane == 0) sRaise[4 * (g & 3) + warp] = raise;
+                __syncwarp();
+                mbar_arrive(&d_full[g & 3]);
+                float s0 = 0.f, s1 = 0.f;
+                auto part = [&](const float(&v)[32], int o, int c) {  // 16 tokens: hi in 8 columns, lo in the next 8
+                    uint32_t hi[8], lo[8];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
+                    for (int e = 0; e < 16; e += 2) {
                         float a, b;
-                        ffma2(v[e], v[e + 1], kLog2e, kLog2e, -Dr, -Dr, a, b);
+                        ffma2(v[o + e], v[o + e + 1], kLog2e, kLog2e, -Dr, -Dr, a, b);
                         a = ex2_approx(a);
                         b = ex2_approx(b);
                         ffma2(a, b, 1.f, 1.f, s0, s1, s0, s1);
                         // hi: the 11 leading bits (exact in fp16 from 2^-14 on), lo: the rest
                         const float ah = tf32_trunc(a), bh_ = tf32_trunc(b);
+                        float al, bl;
+                        ffma2(ah, bh_, -1.f, -1.f, a, b, al, bl);
                         hi[e >> 1] = pack_f16x2(ah, bh_);
-                        lo[e >> 1] = pack_f16x2(a - ah, b - bh_);
+                        lo[e >> 1] = pack_f16x2(al, bl);
                     }
-                    z += s0 + s1;
-                    tmem_st16u(tL + C::T_P + 32 * c, hi);
-                    tmem_st16u(tL + C::T_P + 32 * c + 16, lo);
-                    tmem_wait_st();
-                    tc_fence_before();
-                    mbar_arrive(&phi_full[c]);
+                    tmem_st8u(P + c, hi);
+                    tmem_st8u(P + c + 8, lo);
                 };
-                tmem_wait_ld32(va);
-                tmem_ld32_nowait(tL + C::T_P + 32, vb);
-                chunk(va, 0);
-                tmem_wait_ld32(vb);
-                tmem_ld32_nowait(tL + C::T_P + 64, va);
-                chunk(vb, 1);
-                tmem_wait_ld32(va);
-                tmem_ld32_nowait(tL + C::T_P + 96, vb);
-                chunk(va, 2);
-                tmem_wait_ld32(vb);
-                // b of this tile; seen before the last chunk is handed on, since V's next phase may follow then
-                if (D == 128 && !(ok = mbar_wait_all(&v_conv[g % NS], (g / NS) & 1, abort_flag))) break;
-                chunk(vb, 3);
-                if (D == 128) {
-                    if (!(ok = mbar_wait_all(s_full, g & 1, abort_flag))) break;
-                    tc_fence_after();
-                    flush(g, 64);
-                }
+                part(va, 0, 0);
+                part(va, 16, 16);
+                part(vb, 0, 32);
+                part(vb, 16, 48);
+                z += s0 + s1;
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&phi_full[g & 1]);
             }
             // z', D and the factors that bring the run's S and the carried S' to D
             float2 f = make_float2(0.f, 0.f);
@@ -306,102 +274,196 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 } else {
                     z *= f.x;
                 }
-                if (z != 0.f) dst[(size_t)D * m + m + r] = Dn;
+                if (z != 0.f || !whole) dst[(size_t)D * m + m + r] = Dn;
                 if (z != 0.f || !whole) dst[(size_t)D * m + r] = z;
             }
             sF[row] = f;
             named_bar_sync(2, 256);
-            if (D == 128 && ok) finish(64);
         } else {
-            const int j = threadIdx.x - 128;  // token of the tile
-#pragma unroll
-            for (int c = 0; c < SC; ++c) S[c] = 0.f;
-            // key row j of tile g: -|k|^2/2 in three bf16 parts (their sum has fp32's precision); keys past
-            // the count become zero rows at -inf
+            const int t = threadIdx.x - 128;
+            // key rows of tile g, two threads a row: -|k|^2/2 in three bf16 parts (their sum has fp32's
+            // precision); keys past the count become zero rows at -inf
             auto conv_k = [&](int g) -> bool {
-                const int s = g % NS;
+                const int s = g % NS, j = t >> 1, part = t & 1;
                 if (!mbar_wait_all(&k_full[s], (g / NS) & 1, abort_flag)) return false;
                 uint8_t *kt = sK + (size_t)s * C::KT;
-                uint4 xb = make_uint4(0xFF80u, 0u, 0u, 0u);
-                if ((t0 + g) * kTile + j < count) {
-                    const float h = -0.5f * key_sq_norm<NB, kTile>(kt, j);
-                    if (h >= -3e38f || h != h) {
+                const bool in = (t0 + g) * kExtTile + j < count;
+                float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4 * NB; ++i) {  // chunks of the row: half of one block, or a block each
+                    const int ch = NB == 1 ? 4 * part + i : (i ^ (4 * part));
+                    uint4 *at = (uint4 *)(kt + (NB == 1 ? 0 : part) * C::BLK + sw128_offset(j, ch));
+                    if (in) {
+                        const uint4 x = *at;
+                        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float lo = __uint_as_float(u[k] << 16), hi = __uint_as_float(u[k] & 0xFFFF0000u);
+                            ffma2(lo, hi, lo, hi, a0, a1, a0, a1);
+                        }
+                    } else {
+                        *at = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                float h = a0 + a1;
+                h = -0.5f * (h + __shfl_xor_sync(0xffffffffu, h, 1));
+                if (part == 0) {
+                    uint4 xb = make_uint4(0xFF80u, 0u, 0u, 0u);
+                    if (in && (h >= -3e38f || h != h)) {
                         const uint32_t hi = bf16_bits_rn(h);
                         const float r1 = h - __uint_as_float(hi << 16);
                         const uint32_t mid = bf16_bits_rn(r1);
                         xb = make_uint4(hi | (mid << 16), bf16_bits_rn(r1 - __uint_as_float(mid << 16)), 0u, 0u);
                     }
-                } else {
-                    for (int i = 0; i < 8 * NB; ++i)
-                        *(uint4 *)(kt + (i >> 3) * C::BLK + j * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    *(uint4 *)(sKx + s * C::KX + (j >> 3) * 256 + (j & 7) * 16) = xb;
                 }
-                *(uint4 *)(sKx + s * 4096 + (j >> 3) * 256 + (j & 7) * 16) = xb;
                 fence_async_smem();
                 mbar_arrive(&k_conv[s]);
                 return true;
             };
-            // V tile g to fp16, scaled by its largest finite magnitude (a power of two)
+            // V tile g to fp16 at scale 2^-b: b follows the tiles' largest finite magnitude (which lands in
+            // [2^12, 2^13)) only where it would leave [2^6, 2^15). A bf16 value's fp16 form at that scale is
+            // integer arithmetic on its bits, exact from 2^-14 on (smaller ones are off by 2^-15 at most).
+            int bcur = 0, bnext = 0;  // b of the accumulator, and of the last tile converted
+            bool changed = false;     // the last tile converted changed it
             auto conv_v = [&](int g) -> bool {
                 const int s = g % NS;
                 if (!mbar_wait_all(&v_full[s], (g / NS) & 1, abort_flag)) return false;
                 uint8_t *vt = sV + (size_t)s * C::KT;
-                const int valid = count - (t0 + g) * kTile;
+                const int valid = count - (t0 + g) * kExtTile;
+                uint4 x[4 * NB];
                 uint32_t mx = 0;
-#pragma unroll 4
-                for (int i = 0; i < 8 * NB; ++i) {
-                    const int ch = j + 128 * i;  // 16-byte chunk: row (ch / 8) % 128
-                    if ((ch >> 3) % kTile < valid) {
-                        const uint4 x = *(const uint4 *)(vt + (size_t)ch * 16);
-                        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t a = u[k] & 0x7FFF7FFFu;
-                            mx = __vmaxu2(mx, a & ~__vcmpgeu2(a, 0x7F807F80u));
-                        }
-                    }
+                for (int i = 0; i < 4 * NB; ++i) {
+                    const int c = t + 128 * i;  // 16-byte chunk: row (c / 8) % 64
+                    x[i] = *(const uint4 *)(vt + (size_t)c * 16);
+                    if (valid < kExtTile && (c >> 3) % kExtTile >= valid) x[i] = make_uint4(0u, 0u, 0u, 0u);
+                    const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mx = __vmaxu2(mx, u[k] & 0x7FFF7FFFu);
                 }
-                mx = max(mx & 0xFFFFu, mx >> 16);
-                for (int o = 16; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                mx = __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
                 if (lane == 0) sRed[(g & 1) * 4 + (warp & 3)] = mx;
                 mbar_arrive(v_max);
                 if (!mbar_wait_all(v_max, g & 1, abort_flag)) return false;
-                mx = max(max(sRed[(g & 1) * 4], sRed[(g & 1) * 4 + 1]), max(sRed[(g & 1) * 4 + 2], sRed[(g & 1) * 4 + 3]));
-                const int b = min(max((int)(mx >> 7) - 127 - 7, -100), 120);
-                if (j == 0) sShift[g & 3] = b;
-                const float scale = __uint_as_float((uint32_t)(127 - b) << 23);
-#pragma unroll 4
-                for (int i = 0; i < 8 * NB; ++i) {
-                    const int ch = j + 128 * i;
-                    uint4 *at = (uint4 *)(vt + (size_t)ch * 16);
-                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                    if ((ch >> 3) % kTile < valid) {
-                        x = *at;
-                        uint32_t u[4] = {x.x, x.y, x.z, x.w};
+                const uint4 m4 = *(const uint4 *)(sRed + (g & 1) * 4);
+                mx = max(max(m4.x, m4.y), max(m4.z, m4.w));
+                const bool finite = mx < 0x7F80u;
+                const int b = (int)(mx >> 7) - 127 - 12;
+                changed = g == 0 || !finite || (mx != 0 && (b > bnext + 2 || b < bnext - 6));
+                if (changed) bnext = finite ? min(max(b, -100), 114) : 114;  // (not finite: S is not, either)
+                if (t == 0) sScale[g & 3] = changed;
+                if (finite) {
+                    const uint32_t low = (uint32_t)(112 + bnext) << 7, low2 = low | (low << 16);
+#pragma unroll
+                    for (int i = 0; i < 4 * NB; ++i) {
+                        uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            u[k] = pack_f16x2(__uint_as_float(u[k] << 16) * scale, __uint_as_float(u[k] & 0xFFFF0000u) * scale);
-                        x = make_uint4(u[0], u[1], u[2], u[3]);
+                            u[k] = ((__vmaxu2(u[k] & 0x7FFF7FFFu, low2) - low2) << 3) | (u[k] & 0x80008000u);
+                        *(uint4 *)(vt + (size_t)(t + 128 * i) * 16) = make_uint4(u[0], u[1], u[2], u[3]);
                     }
-                    *at = x;
+                } else {
+                    const float scale = __uint_as_float((uint32_t)(127 - bnext) << 23);
+                    for (int i = 0; i < 4 * NB; ++i) {
+                        uint4 *at = (uint4 *)(vt + (size_t)(t + 128 * i) * 16);
+                        uint32_t u[4] = {at->x, at->y, at->z, at->w};
+                        const bool in = ((t + 128 * i) >> 3) % kExtTile < valid;
+                        for (int k = 0; k < 4; ++k)
+                            u[k] = in ? pack_f16x2(__uint_as_float(u[k] << 16) * scale, __uint_as_float(u[k] & 0xFFFF0000u) * scale) : 0u;
+                        *at = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
                 }
                 fence_async_smem();
                 mbar_arrive(&v_conv[s]);
                 return true;
             };
-            ok = conv_k(0) && conv_v(0);
+            // S_r in units of 2^Dreg: registers at d = 64; at d = 128 the run's partial state in global
+            // memory, 16 columns in flight at a time (128 more registers a thread are not to be had, and
+            // as local memory they took 33,000 cycles a flush)
+            constexpr int SR = D == 64 ? D : 1;
+            float S[SR];
+            float Dreg = 0.f, Dacc = 0.f;  // Dacc: the accumulator's D_r
+            bool first = true;
+#pragma unroll
+            for (int c = 0; c < SR; ++c) S[c] = 0.f;
+            auto flush = [&]() {
+                const float keep = exp2f(fminf(Dreg - Dacc, 0.f));
+                const float up = __uint_as_float((uint32_t)(127 + bcur) << 23);
+                Dreg = Dacc;
+                float v[16];
+                if constexpr (D == 64) {
+#pragma unroll
+                    for (int q = 0; q < D; q += 16) {
+                        tmem_ld16(tL + C::T_ACC + q, v);
+#pragma unroll
+                        for (int c = 0; c < 16; c += 2) {
+                            float a, b;
+                            ffma2(v[c], v[c + 1], up, up, 0.f, 0.f, a, b);
+                            ffma2(S[q + c], S[q + c + 1], keep, keep, a, b, S[q + c], S[q + c + 1]);
+                        }
+                    }
+                } else {
+                    float *at = dst + r, s[16];
+#pragma unroll 1
+                    for (int q = 0; q < D; q += 16, at += 16 * (size_t)m) {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) s[c] = first || r >= m ? 0.f : __ldcg(at + (size_t)c * m);
+                        tmem_ld16(tL + C::T_ACC + q, v);
+                        if (r < m) {
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) __stcg(at + (size_t)c * m, fmaf(s[c], keep, up * v[c]));
+                        }
+                    }
+                    first = false;
+                }
+                tc_fence_before();
+                mbar_arrive(acc_free);
+            };
+            int flushes = 0;
+            ok = conv_k(0) && (n < 2 || conv_k(1)) && conv_v(0);
             for (int g = 0; ok && g < n; ++g) {
-                // the next tile's keys first: its projection waits for them alone
-                if (g + 1 < n) ok = conv_k(g + 1);
-                if (ok && NS > 1 && g + 1 < n) ok = conv_v(g + 1);
-                // (one barrier per parity: the exponent warps may be one tile ahead)
-                if (ok) ok = mbar_wait_all(&d_full[g & 1], (g >> 1) & 1, abort_flag) && mbar_wait_all(s_full, g & 1, abort_flag);
-                if (!ok) break;
+                const int b = bnext;  // of tile g
+                const bool scale = changed;
+                if (g + 2 < n) ok = conv_k(g + 2);
+                if (ok && g + 1 < n) ok = conv_v(g + 1);
+                if (!ok || !(ok = mbar_wait_all(&d_full[g & 3], (g >> 2) & 1, abort_flag))) break;
+                if (g == 0) {
+                    Dacc = sD[row];
+                    bcur = b;
+                    continue;
+                }
+                if (flush_before(g, scale)) {
+                    if (!(ok = mbar_wait_all(acc_full, flushes++ & 1, abort_flag))) break;
+                    tc_fence_after();
+                    flush();
+                    Dacc = sD[(g & 3) * 128 + row];
+                    bcur = b;
+                }
+            }
+            if (ok && (ok = mbar_wait_all(acc_full, flushes & 1, abort_flag))) {
                 tc_fence_after();
-                flush(g, 0);
-                if (NS == 1 && g + 1 < n) ok = conv_v(g + 1);
+                flush();
             }
             named_bar_sync(2, 256);
-            if (ok) finish(0);
+            // the run's S' in the state's units, joined with the carried one
+            // (a partial state is written even where no token entered: the sum over runs reads it)
+            const float2 f = sF[row];
+            if (ok && r < m && (f.x != 0.f || f.y != 0.f || !whole)) {
+#pragma unroll
+                for (int q = 0; q < D; q += 16) {  // 16 columns' loads before their stores
+                    float x[16], y[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const size_t at = (size_t)(q + c) * m + r;
+                        x[c] = D == 64 ? S[D == 64 ? q + c : 0] : __ldcg(dst + at);
+                        y[c] = f.y != 0.f ? __ldcg(old + at) : 0.f;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        dst[(size_t)(q + c) * m + r] = fmaf(y[c], f.y, f.x != 0.f ? x[c] * f.x : 0.f);
+                }
+            }
         }
     }
     tc_fence_before();
@@ -419,7 +481,7 @@ static cudaError_t launch_extend_tc_t(const CUtensorMap &mK, const CUtensorMap &
     if (e != cudaSuccess) return e;
     const int BH = p.B * p.H;
     k_decode_extend_tc<D><<<dim3(p.n_split, (p.m + 127) / 128, BH), C::THREADS, C::BYTES, st>>>(mK, mV, mW, p);
-    if (p.n_split > 1) k_extend_combine<<<dim3(D / kCombCols, BH), p.m, 0, st>>>(p, D);
+    if (p.n_split > 1 || D != 64) k_extend_combine<<<dim3(D / kCombCols, BH), p.m, 0, st>>>(p, D);
     return cudaGetLastError();
 }
 

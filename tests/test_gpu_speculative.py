@@ -237,7 +237,7 @@ def test_extend_matches_oracle(cuda_device, dtype, prior, B, H, L, d, m):
     assert torch.equal(again, state)
 
 
-@pytest.mark.parametrize("L,d,m", [(1300, 64, 256), (1300, 128, 256), (1153, 64, 96), (640, 128, 128), (257, 64, 128)])
+@pytest.mark.parametrize("L,d,m", [(1300, 64, 256), (1300, 128, 256), (1153, 64, 96), (640, 128, 128), (257, 64, 128), (65, 64, 256), (128, 128, 256)])
 def test_extend_runs_of_many_tiles(cuda_device, L, d, m):
     """Enough heads that each takes its tokens in one or two long runs (some heads checked)."""
     B, H = 20, 16
