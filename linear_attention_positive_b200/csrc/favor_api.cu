@@ -1133,7 +1133,7 @@ bool tree_on_tiles(const favor_shape *s) {
 // and the runs each head is cut into.
 //   CUDA cores: up to kExtWhole tokens (an accepted path, a short prompt) one CTA a head updates the
 //   state in place; more are cut so that about four CTAs an SM are in flight.
-//   Tensor cores: as many runs of whole tiles as fill two CTAs an SM once.
+//   Tensor cores: as many runs of whole tiles as fill two CTAs an SM once (d = 128: kExtFlush tiles at most).
 constexpr int kExtWhole = 32;
 constexpr int kExtTcMin = 64;
 struct ExtendPlan {
@@ -1145,7 +1145,9 @@ ExtendPlan extend_plan(const favor_shape *s, int n_tok, bool indexed) {
     if (s->dtype == FAVOR_BF16 && !indexed && n_tok >= kExtTcMin) {
         const long long nt = (n_tok - 1) / kExtTile + 1, rows = BH * ((s->m + 127) / 128);
         const long long runs = std::max<long long>(1, std::min(nt, 2ll * num_sms() / rows));
-        const long long per = (nt + runs - 1) / runs;
+        long long per = (nt + runs - 1) / runs;
+        // at d = 128 a run ends where its accumulator would have to be added up in global memory
+        if (s->d == 128) per = std::min<long long>(per, kExtFlush);
         return {true, (int)((nt + per - 1) / per), (int)(per * kExtTile)};
     }
     if (n_tok <= kExtWhole) return {false, 1, n_tok};

@@ -5,8 +5,8 @@
 //                              products); the norm enters as a K = 16 step of three bf16 parts per key
 //                              against ones columns of W (-inf for a key past the sequence's count);
 //   phi' = 2^(P log2e - D_r)   one thread per feature; D_r, an integer, is set so that the first
-//                              tile's largest exponent lands in (7, 8] and raised whenever a tile's
-//                              passes 15 (fp16 holds 2^t below 2^16);
+//                              tile's largest exponent lands in (2, 3] and raised where a later one's
+//                              passes 15 (fp16 holds 2^t below 2^16; its smallest step is 2^-24);
 //   acc += phi'^T V'           tcgen05 (M = 128, N = d, K = 64), fp16 operands: phi' = hi + lo, two fp16
 //                              values (22 bits), A from TMEM where they replace P; V' = V 2^-b, exact in
 //                              fp16 but for entries 2^-20 of the tile's largest and below (off by 2^-21 of it);
@@ -21,16 +21,17 @@
 // (with one buffer of 128 tokens they did: 283 us for 65536 tokens in 16 heads at d = 64, m = 256).
 // Bound: 2^t on the MUFU (16 a cycle and SM): B H L m of them; next the tensor work, 6 L m d a head.
 //
-// Warps 0-3: exponentials and z_r. Warps 4-7: |k|^2 and the norms' extension, V -> fp16, S. Warp 8: TMA
+// Warps 0-3: exponentials and z_r. Warps 4, 5: |k|^2 and the norms' extension; 6, 7: V -> fp16 (one after
+// the other in all four they held up the exponents: 4200 cycles a tile against 1550); 4-7: S. Warp 8: TMA
 // and MMA issue. Every barrier that a group waits on is at most one phase ahead of it, but d_full, which
-// has four slots: the exponent warps may be two tiles ahead of warps 4-7 there.
+// has four slots: the exponent warps may be two tiles ahead of warps 4-7 there, and warps 6, 7 four of 4, 5.
 
 #include "common.cuh"
 
 namespace favor {
 
 constexpr int kExtTile = 64;
-constexpr int kExtFlush = 8;
+constexpr int kExtFlush = 16;
 
 template <int D_>
 struct ExtTc {
@@ -41,7 +42,7 @@ struct ExtTc {
     static constexpr uint32_t T_P = 0, T_ACC = 128;  // TMEM columns: two tiles of P, the accumulator
     static constexpr size_t OFF_K = WT, OFF_V = OFF_K + NS * KT, OFF_KX = OFF_V + NS * KT, OFF_WX = OFF_KX + NS * KX,
                             OFF_D = OFF_WX + 4096, OFF_F = OFF_D + 4 * 128 * 4, OFF_MISC = OFF_F + 128 * 8,
-                            OFF_BAR = OFF_MISC + 128, BYTES = OFF_BAR + 256 + 1024;
+                            OFF_BAR = OFF_MISC + 4 * (16 + 8 + 8 + 4), BYTES = OFF_BAR + 256 + 1024;
 };
 
 template <int D>
@@ -56,8 +57,8 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
     float *sD = (float *)(smem + C::OFF_D);       // [tile % 4][128]: D_r
     float2 *sF = (float2 *)(smem + C::OFF_F);     // [128]: final factors of the run's and the old S'
     int *sRaise = (int *)(smem + C::OFF_MISC);    // [tile % 4][warp]: some D_r of this warp's changes here
-    int *sScale = sRaise + 16;                    // [tile % 4]: b changes here
-    uint32_t *sRed = (uint32_t *)(sScale + 4);    // [2][4]
+    int *sScale = sRaise + 16, *sB = sScale + 8;  // [tile % 8]: b changes here; b
+    uint32_t *sRed = (uint32_t *)(sB + 8);        // [2][2]
     uint64_t *bars = (uint64_t *)(smem + C::OFF_BAR);
     uint64_t *k_full = bars, *v_full = k_full + NS, *k_conv = v_full + NS, *v_conv = k_conv + NS;
     uint64_t *p_full = v_conv + NS, *phi_full = p_full + 2, *s_done = phi_full + 2, *d_full = s_done + 2;
@@ -81,19 +82,19 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
         for (int s = 0; s < NS; ++s) {
             mbar_init(&k_full[s], 1);
             mbar_init(&v_full[s], 1);
-            mbar_init(&k_conv[s], 128);
-            mbar_init(&v_conv[s], 128);
+            mbar_init(&k_conv[s], 64);
+            mbar_init(&v_conv[s], 64);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&p_full[s], 1);
             mbar_init(&phi_full[s], 128);
             mbar_init(&s_done[s], 1);
         }
-        for (int s = 0; s < 4; ++s) mbar_init(&d_full[s], 128);
+        for (int s = 0; s < 4; ++s) mbar_init(&d_full[s], 192);
         mbar_init(w_full, 1);
         mbar_init(acc_full, 1);
         mbar_init(acc_free, 128);
-        mbar_init(v_max, 128);
+        mbar_init(v_max, 64);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -115,11 +116,11 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // whether S takes the accumulator before tile g adds to it (read after tile g's d_full or phi_full);
-    // scale: b changes with tile g
-    auto flush_before = [&](int g, bool scale) {
+    // whether S takes the accumulator before tile g adds to it (read after tile g's d_full, or its phi_full
+    // and v_conv)
+    auto flush_before = [&](int g) {
         const int *r = sRaise + 4 * (g & 3);
-        return g > 0 && ((g % kExtFlush) == 0 || scale || (r[0] | r[1] | r[2] | r[3]) != 0);
+        return g > 0 && ((g % kExtFlush) == 0 || sScale[g & 7] != 0 || (r[0] | r[1] | r[2] | r[3]) != 0);
     };
 
     if (warp == 8) {
@@ -172,7 +173,7 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                      mbar_wait_all(&phi_full[j & 1], (j >> 1) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                const bool fresh = flush_before(j, sScale[j & 3] != 0);
+                const bool fresh = flush_before(j);
                 if (fresh) {
                     mma_commit_w(acc_full);
                     if (!(ok = mbar_wait_all(acc_free, flushes++ & 1, abort_flag))) break;
@@ -216,7 +217,7 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 const float um = fmaxf(chunk_vmax(va), chunk_vmax(vb)), tm = um * kLog2e;
                 bool raise = false;
                 if (tm > -INFINITY && (umax == -INFINITY || tm - Dr > 15.f)) {
-                    const float Dn = ceilf(tm) - 8.f;
+                    const float Dn = ceilf(tm) - 3.f;
                     z = z == 0.f ? 0.f : z * exp2f(Dr - Dn);
                     Dr = Dn;
                     raise = true;
@@ -280,97 +281,83 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             sF[row] = f;
             named_bar_sync(2, 256);
         } else {
-            const int t = threadIdx.x - 128;
-            // key rows of tile g, two threads a row: -|k|^2/2 in three bf16 parts (their sum has fp32's
+            // Warps 4 and 5, key rows of tile g, one a thread: -|k|^2/2 in three bf16 parts (their sum has fp32's
             // precision); keys past the count become zero rows at -inf
             auto conv_k = [&](int g) -> bool {
-                const int s = g % NS, j = t >> 1, part = t & 1;
+                const int s = g % NS, j = threadIdx.x - 128;
                 if (!mbar_wait_all(&k_full[s], (g / NS) & 1, abort_flag)) return false;
                 uint8_t *kt = sK + (size_t)s * C::KT;
-                const bool in = (t0 + g) * kExtTile + j < count;
-                float a0 = 0.f, a1 = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4 * NB; ++i) {  // chunks of the row: half of one block, or a block each
-                    const int ch = NB == 1 ? 4 * part + i : (i ^ (4 * part));
-                    uint4 *at = (uint4 *)(kt + (NB == 1 ? 0 : part) * C::BLK + sw128_offset(j, ch));
-                    if (in) {
-                        const uint4 x = *at;
-                        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float lo = __uint_as_float(u[k] << 16), hi = __uint_as_float(u[k] & 0xFFFF0000u);
-                            ffma2(lo, hi, lo, hi, a0, a1, a0, a1);
-                        }
-                    } else {
-                        *at = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                }
-                float h = a0 + a1;
-                h = -0.5f * (h + __shfl_xor_sync(0xffffffffu, h, 1));
-                if (part == 0) {
-                    uint4 xb = make_uint4(0xFF80u, 0u, 0u, 0u);
-                    if (in && (h >= -3e38f || h != h)) {
+                uint4 xb = make_uint4(0xFF80u, 0u, 0u, 0u);
+                if ((t0 + g) * kExtTile + j < count) {
+                    const float h = -0.5f * key_sq_norm<NB, kExtTile>(kt, j);
+                    if (h >= -3e38f || h != h) {
                         const uint32_t hi = bf16_bits_rn(h);
                         const float r1 = h - __uint_as_float(hi << 16);
                         const uint32_t mid = bf16_bits_rn(r1);
                         xb = make_uint4(hi | (mid << 16), bf16_bits_rn(r1 - __uint_as_float(mid << 16)), 0u, 0u);
                     }
-                    *(uint4 *)(sKx + s * C::KX + (j >> 3) * 256 + (j & 7) * 16) = xb;
+                } else {
+                    for (int i = 0; i < 8 * NB; ++i)
+                        *(uint4 *)(kt + (i >> 3) * C::BLK + j * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
+                *(uint4 *)(sKx + s * C::KX + (j >> 3) * 256 + (j & 7) * 16) = xb;
                 fence_async_smem();
                 mbar_arrive(&k_conv[s]);
                 return true;
             };
-            // V tile g to fp16 at scale 2^-b: b follows the tiles' largest finite magnitude (which lands in
+            // Warps 6 and 7, V tile g to fp16 at scale 2^-b: b follows the tiles' largest finite magnitude (which lands in
             // [2^12, 2^13)) only where it would leave [2^6, 2^15). A bf16 value's fp16 form at that scale is
             // integer arithmetic on its bits, exact from 2^-14 on (smaller ones are off by 2^-15 at most).
-            int bcur = 0, bnext = 0;  // b of the accumulator, and of the last tile converted
-            bool changed = false;     // the last tile converted changed it
+            const int t = threadIdx.x - 192;
+            int bnext = 0;  // b of the last tile converted
             auto conv_v = [&](int g) -> bool {
                 const int s = g % NS;
                 if (!mbar_wait_all(&v_full[s], (g / NS) & 1, abort_flag)) return false;
                 uint8_t *vt = sV + (size_t)s * C::KT;
                 const int valid = count - (t0 + g) * kExtTile;
-                uint4 x[4 * NB];
                 uint32_t mx = 0;
-#pragma unroll
-                for (int i = 0; i < 4 * NB; ++i) {
-                    const int c = t + 128 * i;  // 16-byte chunk: row (c / 8) % 64
-                    x[i] = *(const uint4 *)(vt + (size_t)c * 16);
-                    if (valid < kExtTile && (c >> 3) % kExtTile >= valid) x[i] = make_uint4(0u, 0u, 0u, 0u);
-                    const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll 4
+                for (int i = 0; i < 8 * NB; ++i) {
+                    const int c = t + 64 * i;  // 16-byte chunk: row (c / 8) % 64
+                    uint4 *at = (uint4 *)(vt + (size_t)c * 16);
+                    if (valid < kExtTile && (c >> 3) % kExtTile >= valid) *at = make_uint4(0u, 0u, 0u, 0u);
+                    const uint4 x = *at;
+                    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) mx = __vmaxu2(mx, u[k] & 0x7FFF7FFFu);
                 }
                 mx = __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
-                if (lane == 0) sRed[(g & 1) * 4 + (warp & 3)] = mx;
+                if (lane == 0) sRed[(g & 1) * 2 + (warp & 1)] = mx;
                 mbar_arrive(v_max);
                 if (!mbar_wait_all(v_max, g & 1, abort_flag)) return false;
-                const uint4 m4 = *(const uint4 *)(sRed + (g & 1) * 4);
-                mx = max(max(m4.x, m4.y), max(m4.z, m4.w));
+                mx = max(sRed[(g & 1) * 2], sRed[(g & 1) * 2 + 1]);
                 const bool finite = mx < 0x7F80u;
                 const int b = (int)(mx >> 7) - 127 - 12;
-                changed = g == 0 || !finite || (mx != 0 && (b > bnext + 2 || b < bnext - 6));
+                const bool changed = g == 0 || !finite || (mx != 0 && (b > bnext + 2 || b < bnext - 6));
                 if (changed) bnext = finite ? min(max(b, -100), 114) : 114;  // (not finite: S is not, either)
-                if (t == 0) sScale[g & 3] = changed;
+                if (t == 0) {
+                    sScale[g & 7] = changed;
+                    sB[g & 7] = bnext;
+                }
+                mbar_arrive(&d_full[g & 3]);
                 if (finite) {
                     const uint32_t low = (uint32_t)(112 + bnext) << 7, low2 = low | (low << 16);
-#pragma unroll
-                    for (int i = 0; i < 4 * NB; ++i) {
-                        uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll 4
+                    for (int i = 0; i < 8 * NB; ++i) {
+                        const uint4 x = *(const uint4 *)(vt + (size_t)(t + 64 * i) * 16);
+                        uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             u[k] = ((__vmaxu2(u[k] & 0x7FFF7FFFu, low2) - low2) << 3) | (u[k] & 0x80008000u);
-                        *(uint4 *)(vt + (size_t)(t + 128 * i) * 16) = make_uint4(u[0], u[1], u[2], u[3]);
+                        *(uint4 *)(vt + (size_t)(t + 64 * i) * 16) = make_uint4(u[0], u[1], u[2], u[3]);
                     }
                 } else {
                     const float scale = __uint_as_float((uint32_t)(127 - bnext) << 23);
-                    for (int i = 0; i < 4 * NB; ++i) {
-                        uint4 *at = (uint4 *)(vt + (size_t)(t + 128 * i) * 16);
+                    for (int i = 0; i < 8 * NB; ++i) {
+                        uint4 *at = (uint4 *)(vt + (size_t)(t + 64 * i) * 16);
                         uint32_t u[4] = {at->x, at->y, at->z, at->w};
-                        const bool in = ((t + 128 * i) >> 3) % kExtTile < valid;
                         for (int k = 0; k < 4; ++k)
-                            u[k] = in ? pack_f16x2(__uint_as_float(u[k] << 16) * scale, __uint_as_float(u[k] & 0xFFFF0000u) * scale) : 0u;
+                            u[k] = pack_f16x2(__uint_as_float(u[k] << 16) * scale, __uint_as_float(u[k] & 0xFFFF0000u) * scale);
                         *at = make_uint4(u[0], u[1], u[2], u[3]);
                     }
                 }
@@ -383,7 +370,8 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             // as local memory they took 33,000 cycles a flush)
             constexpr int SR = D == 64 ? D : 1;
             float S[SR];
-            float Dreg = 0.f, Dacc = 0.f;  // Dacc: the accumulator's D_r
+            float Dreg = 0.f, Dacc = 0.f;  // Dacc, bcur: the accumulator's D_r and b
+            int bcur = 0;
             bool first = true;
 #pragma unroll
             for (int c = 0; c < SR; ++c) S[c] = 0.f;
@@ -420,25 +408,24 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 tc_fence_before();
                 mbar_arrive(acc_free);
             };
+            const bool keys = warp < 6;
             int flushes = 0;
-            ok = conv_k(0) && (n < 2 || conv_k(1)) && conv_v(0);
+            ok = keys ? conv_k(0) && (n < 2 || conv_k(1)) : conv_v(0);
             for (int g = 0; ok && g < n; ++g) {
-                const int b = bnext;  // of tile g
-                const bool scale = changed;
-                if (g + 2 < n) ok = conv_k(g + 2);
-                if (ok && g + 1 < n) ok = conv_v(g + 1);
+                if (keys)
+                    ok = g + 2 >= n || conv_k(g + 2);
+                else
+                    ok = g + 1 >= n || conv_v(g + 1);
                 if (!ok || !(ok = mbar_wait_all(&d_full[g & 3], (g >> 2) & 1, abort_flag))) break;
-                if (g == 0) {
-                    Dacc = sD[row];
-                    bcur = b;
-                    continue;
-                }
-                if (flush_before(g, scale)) {
+                const bool take = flush_before(g);
+                if (take) {
                     if (!(ok = mbar_wait_all(acc_full, flushes++ & 1, abort_flag))) break;
                     tc_fence_after();
                     flush();
+                }
+                if (take || g == 0) {
                     Dacc = sD[(g & 3) * 128 + row];
-                    bcur = b;
+                    bcur = sB[g & 7];
                 }
             }
             if (ok && (ok = mbar_wait_all(acc_full, flushes & 1, abort_flag))) {
