@@ -22,8 +22,8 @@
 // Bound: 2^t on the MUFU (16 a cycle and SM): B H L m of them; next the tensor work, 6 L m d a head.
 //
 // Warps 0-3: exponentials and z_r. Warps 4, 5: |k|^2 and the norms' extension; 6, 7: V -> fp16 (one after
-// the other in all four they held up the exponents: 4200 cycles a tile against 1550); 4-7: S. Warp 8: TMA
-// and MMA issue. Every barrier that a group waits on is at most one phase ahead of it, but d_full, which
+// the other in all four they held up the exponents: 4200 cycles a tile against 1550); 4-7: S. Warp 8: K
+// and W copies, P; warp 9: V copies, the accumulator. Every barrier that a group waits on is at most one phase ahead of it, but d_full, which
 // has four slots: the exponent warps may be two tiles ahead of warps 4-7 there, and warps 6, 7 four of 4, 5.
 
 #include "common.cuh"
@@ -38,11 +38,11 @@ struct ExtTc {
     static constexpr int D = D_, NB = D / 64;
     static constexpr int NS = D == 64 ? 4 : 2;  // K and V stages each (227 KB for two CTAs)
     static constexpr uint32_t WBLK = 128 * 128, WT = NB * WBLK, BLK = kExtTile * 128, KT = NB * BLK, KX = kExtTile * 32;
-    static constexpr int THREADS = 288;
+    static constexpr int THREADS = 320;
     static constexpr uint32_t T_P = 0, T_ACC = 128;  // TMEM columns: two tiles of P, the accumulator
     static constexpr size_t OFF_K = WT, OFF_V = OFF_K + NS * KT, OFF_KX = OFF_V + NS * KT, OFF_WX = OFF_KX + NS * KX,
                             OFF_D = OFF_WX + 4096, OFF_F = OFF_D + 4 * 128 * 4, OFF_MISC = OFF_F + 128 * 8,
-                            OFF_BAR = OFF_MISC + 4 * (16 + 8 + 8 + 4), BYTES = OFF_BAR + 256 + 1024;
+                            OFF_BAR = OFF_MISC + 4 * (16 + 8 + 8 + 4), BYTES = OFF_BAR + 8 * (4 * NS + 2 + 2 + 2 + 4 + 6) + 8 + 1024;
 };
 
 template <int D>
@@ -63,7 +63,7 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
     uint64_t *k_full = bars, *v_full = k_full + NS, *k_conv = v_full + NS, *v_conv = k_conv + NS;
     uint64_t *p_full = v_conv + NS, *phi_full = p_full + 2, *s_done = phi_full + 2, *d_full = s_done + 2;
     uint64_t *w_full = d_full + 4, *acc_full = w_full + 1, *acc_free = w_full + 2, *v_max = w_full + 3, *drain = w_full + 4;
-    uint32_t *tmem_slot = (uint32_t *)(drain + 1);
+    uint32_t *tmem_slot = (uint32_t *)(drain + 2);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -95,7 +95,8 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
         mbar_init(acc_full, 1);
         mbar_init(acc_free, 128);
         mbar_init(v_max, 64);
-        mbar_init(drain, 1);
+        mbar_init(&drain[0], 1);
+        mbar_init(&drain[1], 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -123,16 +124,16 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
         return g > 0 && ((g % kExtFlush) == 0 || sScale[g & 7] != 0 || (r[0] | r[1] | r[2] | r[3]) != 0);
     };
 
-    if (warp == 8) {
-        auto load = [&](const CUtensorMap *map, uint8_t *buf, uint64_t *bar, int g) {
-            if (elect_one()) {
-                mbar_arrive_expect_tx(&bar[g % NS], C::KT);
-                for (int nb = 0; nb < NB; ++nb)
-                    tma_load_3d(buf + (size_t)(g % NS) * C::KT + nb * C::BLK, map, &bar[g % NS], 64 * nb, (t0 + g) * kExtTile, bh);
-            }
-            __syncwarp();
-        };
-        int nk = 0, nv = 0;  // K and V tiles asked for
+    auto load = [&](const CUtensorMap *map, uint8_t *buf, uint64_t *bar, int g) {
+        if (elect_one()) {
+            mbar_arrive_expect_tx(&bar[g % NS], C::KT);
+            for (int nb = 0; nb < NB; ++nb)
+                tma_load_3d(buf + (size_t)(g % NS) * C::KT + nb * C::BLK, map, &bar[g % NS], 64 * nb, (t0 + g) * kExtTile, bh);
+        }
+        __syncwarp();
+    };
+    if (warp == 8) {  // K and W copies, P
+        int nk = 0;  // K tiles asked for
         load(&mapK, sK, k_full, nk++);
         if (elect_one()) {
             mbar_arrive_expect_tx(w_full, C::WT);
@@ -140,62 +141,67 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
         }
         __syncwarp();
         for (; nk < min(NS, n); ++nk) load(&mapK, sK, k_full, nk);
-        for (; nv < min(NS, n); ++nv) load(&mapV, sV, v_full, nv);
-        const uint32_t idesc_p = make_idesc(128, kExtTile, kFmtBF16, 0, 0), idesc_s = make_idesc(128, D, kFmtF16, 0, 1);
+        const uint32_t idesc_p = make_idesc(128, kExtTile, kFmtBF16, 0, 0);
         const uint64_t dW = make_sdesc(smem_u32(sW), 16, 1024), dK = make_sdesc(smem_u32(sK), 16, 1024);
-        const uint64_t dV = make_sdesc(smem_u32(sV), C::BLK, 1024);
         const uint64_t dWx = make_sdesc_interleaved(smem_u32(sWx), 128, 256);
         const uint64_t dKx = make_sdesc_interleaved(smem_u32(sKx), 128, 256);
         bool ok = mbar_wait_all(w_full, 0, abort_flag);
-        int flushes = 0;
-        for (int i = 0; ok && i <= n; ++i) {
-            if (i < n) {  // P of tile i, where phi' of tile i - 2 was
-                const int s = i % NS;
-                if (i >= 2) {
-                    if (!(ok = mbar_wait_all(&s_done[i & 1], ((i >> 1) - 1) & 1, abort_flag))) break;
-                    if (nv < n) load(&mapV, sV, v_full, nv++);
-                }
-                if (!(ok = mbar_wait_all(&k_conv[s], (i / NS) & 1, abort_flag))) break;
-                tc_fence_after();
-                const uint32_t P = tmem + C::T_P + kExtTile * (i & 1);
-                for (int nb = 0; nb < NB; ++nb)
-                    mma_ss_x4_w(P, dW + nb * (C::WBLK / 16), dK + s * (C::KT / 16) + nb * (C::BLK / 16), idesc_p, nb > 0, 2, 2);
-                mma_f16_ss_w(P, dWx, dKx + s * (C::KX / 16), idesc_p, 1u);
-                mma_commit_w(&p_full[i & 1]);
-            }
-            if (i >= 1) {  // S of tile i - 1
-                const int j = i - 1;
-                if (nk < n) {  // its keys are done with
-                    if (!(ok = mbar_wait_all(&p_full[j & 1], (j >> 1) & 1, abort_flag))) break;
-                    load(&mapK, sK, k_full, nk++);
-                }
-                ok = mbar_wait_all(&v_conv[j % NS], (j / NS) & 1, abort_flag) &&
-                     mbar_wait_all(&phi_full[j & 1], (j >> 1) & 1, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-                const bool fresh = flush_before(j);
-                if (fresh) {
-                    mma_commit_w(acc_full);
-                    if (!(ok = mbar_wait_all(acc_free, flushes++ & 1, abort_flag))) break;
-                    tc_fence_after();
-                }
-                const uint32_t phi = tmem + C::T_P + kExtTile * (j & 1);
-                const uint64_t v = dV + (j % NS) * (C::KT / 16);
-#pragma unroll
-                for (int k = 0; k < kExtTile / 16; ++k) {
-                    mma_f16_ts_w(tmem + C::T_ACC, phi + 16 * k, v + k * (16 * 128 / 16), idesc_s, !(j == 0 || fresh) || k > 0);
-                    mma_f16_ts_w(tmem + C::T_ACC, phi + 16 * k + 8, v + k * (16 * 128 / 16), idesc_s, 1u);
-                }
-                mma_commit_w(&s_done[j & 1]);
+        for (int i = 0; ok && i < n; ++i) {  // where phi' of tile i - 2 was
+            const int s = i % NS;
+            ok = mbar_wait_all(&k_conv[s], (i / NS) & 1, abort_flag) &&
+                 (i < 2 || mbar_wait_all(&s_done[i & 1], ((i >> 1) - 1) & 1, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t P = tmem + C::T_P + kExtTile * (i & 1);
+            for (int nb = 0; nb < NB; ++nb)
+                mma_ss_x4_w(P, dW + nb * (C::WBLK / 16), dK + s * (C::KT / 16) + nb * (C::BLK / 16), idesc_p, nb > 0, 2, 2);
+            mma_f16_ss_w(P, dWx, dKx + s * (C::KX / 16), idesc_p, 1u);
+            mma_commit_w(&p_full[i & 1]);
+            if (i >= 1 && nk < n) {  // the keys of the tile before are done with
+                if (!(ok = mbar_wait_all(&p_full[(i - 1) & 1], ((i - 1) >> 1) & 1, abort_flag))) break;
+                load(&mapK, sK, k_full, nk++);
             }
         }
-        if (ok) mma_commit_w(acc_full);
-        // nothing of this CTA is in flight when it frees its memory
-        mma_commit_w(drain);
+        // nothing of this warp is in flight when the CTA frees its memory
+        mma_commit_w(&drain[0]);
         volatile int no_abort = 0;
-        mbar_wait_all(drain, 0, &no_abort);
+        mbar_wait_all(&drain[0], 0, &no_abort);
         mbar_wait_all(w_full, 0, &no_abort);
         for (int g = max(nk - NS, 0); g < nk; ++g) mbar_wait_all(&k_full[g % NS], (g / NS) & 1, &no_abort);
+    } else if (warp == 9) {  // V copies, S
+        int nv = 0, flushes = 0;  // V tiles asked for
+        for (; nv < min(NS, n); ++nv) load(&mapV, sV, v_full, nv);
+        const uint32_t idesc_s = make_idesc(128, D, kFmtF16, 0, 1);
+        const uint64_t dV = make_sdesc(smem_u32(sV), C::BLK, 1024);
+        bool ok = true;
+        for (int j = 0; ok && j < n; ++j) {
+            if (j >= 1 && nv < n) {  // the values of the tile before are done with
+                if (!(ok = mbar_wait_all(&s_done[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag))) break;
+                load(&mapV, sV, v_full, nv++);
+            }
+            ok = mbar_wait_all(&v_conv[j % NS], (j / NS) & 1, abort_flag) &&
+                 mbar_wait_all(&phi_full[j & 1], (j >> 1) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const bool fresh = flush_before(j);
+            if (fresh) {
+                mma_commit_w(acc_full);
+                if (!(ok = mbar_wait_all(acc_free, flushes++ & 1, abort_flag))) break;
+                tc_fence_after();
+            }
+            const uint32_t phi = tmem + C::T_P + kExtTile * (j & 1);
+            const uint64_t v = dV + (j % NS) * (C::KT / 16);
+#pragma unroll
+            for (int k = 0; k < kExtTile / 16; ++k) {
+                mma_f16_ts_w(tmem + C::T_ACC, phi + 16 * k, v + k * (16 * 128 / 16), idesc_s, !(j == 0 || fresh) || k > 0);
+                mma_f16_ts_w(tmem + C::T_ACC, phi + 16 * k + 8, v + k * (16 * 128 / 16), idesc_s, 1u);
+            }
+            mma_commit_w(&s_done[j & 1]);
+        }
+        if (ok) mma_commit_w(acc_full);
+        mma_commit_w(&drain[1]);
+        volatile int no_abort = 0;
+        mbar_wait_all(&drain[1], 0, &no_abort);
         for (int g = max(nv - NS, 0); g < nv; ++g) mbar_wait_all(&v_full[g % NS], (g / NS) & 1, &no_abort);
     } else {
         const int row = (warp & 3) * 32 + lane, r = half * 128 + row;
@@ -315,16 +321,22 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 if (!mbar_wait_all(&v_full[s], (g / NS) & 1, abort_flag)) return false;
                 uint8_t *vt = sV + (size_t)s * C::KT;
                 const int valid = count - (t0 + g) * kExtTile;
+                // (16-byte chunks t, t + 64, ..: row (c / 8) % 64; eight loads before what uses them)
+                if (valid < kExtTile)
+                    for (int c = t; c < 512 * NB; c += 64)
+                        if ((c >> 3) % kExtTile >= valid) *(uint4 *)(vt + (size_t)c * 16) = make_uint4(0u, 0u, 0u, 0u);
                 uint32_t mx = 0;
-#pragma unroll 4
-                for (int i = 0; i < 8 * NB; ++i) {
-                    const int c = t + 64 * i;  // 16-byte chunk: row (c / 8) % 64
-                    uint4 *at = (uint4 *)(vt + (size_t)c * 16);
-                    if (valid < kExtTile && (c >> 3) % kExtTile >= valid) *at = make_uint4(0u, 0u, 0u, 0u);
-                    const uint4 x = *at;
-                    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll 1
+                for (int nb = 0; nb < NB; ++nb) {
+                    uint4 x[8];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mx = __vmaxu2(mx, u[k] & 0x7FFF7FFFu);
+                    for (int i = 0; i < 8; ++i) x[i] = *(const uint4 *)(vt + (size_t)(t + 64 * (8 * nb + i)) * 16);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t a = __vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu);
+                        const uint32_t b = __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu);
+                        mx = __vmaxu2(mx, __vmaxu2(a, b));
+                    }
                 }
                 mx = __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
                 if (lane == 0) sRed[(g & 1) * 2 + (warp & 1)] = mx;
@@ -342,14 +354,19 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 mbar_arrive(&d_full[g & 3]);
                 if (finite) {
                     const uint32_t low = (uint32_t)(112 + bnext) << 7, low2 = low | (low << 16);
-#pragma unroll 4
-                    for (int i = 0; i < 8 * NB; ++i) {
-                        const uint4 x = *(const uint4 *)(vt + (size_t)(t + 64 * i) * 16);
-                        uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll 1
+                    for (int nb = 0; nb < NB; ++nb) {
+                        uint4 x[8];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            u[k] = ((__vmaxu2(u[k] & 0x7FFF7FFFu, low2) - low2) << 3) | (u[k] & 0x80008000u);
-                        *(uint4 *)(vt + (size_t)(t + 64 * i) * 16) = make_uint4(u[0], u[1], u[2], u[3]);
+                        for (int i = 0; i < 8; ++i) x[i] = *(const uint4 *)(vt + (size_t)(t + 64 * (8 * nb + i)) * 16);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                u[k] = ((__vmaxu2(u[k] & 0x7FFF7FFFu, low2) - low2) << 3) | (u[k] & 0x80008000u);
+                            *(uint4 *)(vt + (size_t)(t + 64 * (8 * nb + i)) * 16) = make_uint4(u[0], u[1], u[2], u[3]);
+                        }
                     }
                 } else {
                     const float scale = __uint_as_float((uint32_t)(127 - bnext) << 23);
