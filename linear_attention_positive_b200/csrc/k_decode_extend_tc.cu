@@ -24,7 +24,7 @@
 // Warps 0-3: exponentials and z_r. Warps 4, 5: |k|^2 and the norms' extension; 6, 7: V -> fp16 (one after
 // the other in all four they held up the exponents: 4200 cycles a tile against 1550); 4-7: S. Warp 8: K
 // and W copies, P; warp 9: V copies, the accumulator. Every barrier that a group waits on is at most one phase ahead of it, but d_full, which
-// has four slots: the exponent warps may be two tiles ahead of warps 4-7 there, and warps 6, 7 four of 4, 5.
+// has four slots: the exponent warps may be two tiles ahead of warps 4-7 there, warps 6, 7 four of 4, 5.
 
 #include "common.cuh"
 
@@ -42,7 +42,7 @@ struct ExtTc {
     static constexpr uint32_t T_P = 0, T_ACC = 128;  // TMEM columns: two tiles of P, the accumulator
     static constexpr size_t OFF_K = WT, OFF_V = OFF_K + NS * KT, OFF_KX = OFF_V + NS * KT, OFF_WX = OFF_KX + NS * KX,
                             OFF_D = OFF_WX + 4096, OFF_F = OFF_D + 4 * 128 * 4, OFF_MISC = OFF_F + 128 * 8,
-                            OFF_BAR = OFF_MISC + 4 * (16 + 8 + 8 + 4), BYTES = OFF_BAR + 8 * (4 * NS + 2 + 2 + 2 + 4 + 6) + 8 + 1024;
+                            OFF_BAR = OFF_MISC + 4 * (16 + 8 + 8), BYTES = OFF_BAR + 8 * (4 * NS + 2 + 2 + 2 + 4 + 5 + 4) + 8 + 1024;
 };
 
 template <int D>
@@ -58,12 +58,11 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
     float2 *sF = (float2 *)(smem + C::OFF_F);     // [128]: final factors of the run's and the old S'
     int *sRaise = (int *)(smem + C::OFF_MISC);    // [tile % 4][warp]: some D_r of this warp's changes here
     int *sScale = sRaise + 16, *sB = sScale + 8;  // [tile % 8]: b changes here; b
-    uint32_t *sRed = (uint32_t *)(sB + 8);        // [2][2]
     uint64_t *bars = (uint64_t *)(smem + C::OFF_BAR);
     uint64_t *k_full = bars, *v_full = k_full + NS, *k_conv = v_full + NS, *v_conv = k_conv + NS;
     uint64_t *p_full = v_conv + NS, *phi_full = p_full + 2, *s_done = phi_full + 2, *d_full = s_done + 2;
-    uint64_t *w_full = d_full + 4, *acc_full = w_full + 1, *acc_free = w_full + 2, *v_max = w_full + 3, *drain = w_full + 4;
-    uint32_t *tmem_slot = (uint32_t *)(drain + 2);
+    uint64_t *w_full = d_full + 4, *acc_full = w_full + 1, *acc_free = w_full + 2, *drain = w_full + 3, *b_set = w_full + 5;
+    uint32_t *tmem_slot = (uint32_t *)(b_set + 4);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -83,18 +82,20 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             mbar_init(&k_full[s], 1);
             mbar_init(&v_full[s], 1);
             mbar_init(&k_conv[s], 64);
-            mbar_init(&v_conv[s], 64);
+            mbar_init(&v_conv[s], 32);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&p_full[s], 1);
             mbar_init(&phi_full[s], 128);
             mbar_init(&s_done[s], 1);
         }
-        for (int s = 0; s < 4; ++s) mbar_init(&d_full[s], 192);
+        for (int s = 0; s < 4; ++s) {
+            mbar_init(&d_full[s], 160);
+            mbar_init(&b_set[s], 32);
+        }
         mbar_init(w_full, 1);
         mbar_init(acc_full, 1);
         mbar_init(acc_free, 128);
-        mbar_init(v_max, 64);
         mbar_init(&drain[0], 1);
         mbar_init(&drain[1], 1);
         *abort_flag = 0;
@@ -235,12 +236,15 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 __syncwarp();
                 mbar_arrive(&d_full[g & 3]);
                 float s0 = 0.f, s1 = 0.f;
-                auto part = [&](const float(&v)[32], int o, int c) {  // 16 tokens: hi in 8 columns, lo in the next 8
+#pragma unroll 1
+                for (int c = 0; c < kExtTile; c += 16) {  // 16 tokens: hi in 8 columns, lo in the next 8
+                    float v[16];
+                    tmem_ld16(P + c, v);
                     uint32_t hi[8], lo[8];
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
                         float a, b;
-                        ffma2(v[o + e], v[o + e + 1], kLog2e, kLog2e, -Dr, -Dr, a, b);
+                        ffma2(v[e], v[e + 1], kLog2e, kLog2e, -Dr, -Dr, a, b);
                         a = ex2_approx(a);
                         b = ex2_approx(b);
                         ffma2(a, b, 1.f, 1.f, s0, s1, s0, s1);
@@ -253,11 +257,7 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                     }
                     tmem_st8u(P + c, hi);
                     tmem_st8u(P + c + 8, lo);
-                };
-                part(va, 0, 0);
-                part(va, 16, 16);
-                part(vb, 0, 32);
-                part(vb, 16, 48);
+                }
                 z += s0 + s1;
                 tmem_wait_st();
                 tc_fence_before();
@@ -311,67 +311,68 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 mbar_arrive(&k_conv[s]);
                 return true;
             };
-            // Warps 6 and 7, V tile g to fp16 at scale 2^-b: b follows the tiles' largest finite magnitude (which lands in
+            // Warps 6 and 7 in turn, V tile g to fp16 at scale 2^-b: b follows the tiles' largest finite magnitude (which lands in
             // [2^12, 2^13)) only where it would leave [2^6, 2^15). A bf16 value's fp16 form at that scale is
             // integer arithmetic on its bits, exact from 2^-14 on (smaller ones are off by 2^-15 at most).
-            const int t = threadIdx.x - 192;
-            int bnext = 0;  // b of the last tile converted
             auto conv_v = [&](int g) -> bool {
                 const int s = g % NS;
                 if (!mbar_wait_all(&v_full[s], (g / NS) & 1, abort_flag)) return false;
                 uint8_t *vt = sV + (size_t)s * C::KT;
                 const int valid = count - (t0 + g) * kExtTile;
-                // (16-byte chunks t, t + 64, ..: row (c / 8) % 64; eight loads before what uses them)
+                // (16-byte chunks lane, lane + 32, ..: row (c / 8) % 64; four loads before what uses them)
                 if (valid < kExtTile)
-                    for (int c = t; c < 512 * NB; c += 64)
+                    for (int c = lane; c < 512 * NB; c += 32)
                         if ((c >> 3) % kExtTile >= valid) *(uint4 *)(vt + (size_t)c * 16) = make_uint4(0u, 0u, 0u, 0u);
                 uint32_t mx = 0;
 #pragma unroll 1
-                for (int nb = 0; nb < NB; ++nb) {
-                    uint4 x[8];
+                for (int q = 0; q < 4 * NB; ++q) {
+                    uint4 x[4];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = *(const uint4 *)(vt + (size_t)(t + 64 * (8 * nb + i)) * 16);
+                    for (int i = 0; i < 4; ++i) x[i] = *(const uint4 *)(vt + (size_t)(lane + 32 * (4 * q + i)) * 16);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < 4; ++i) {
                         const uint32_t a = __vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu);
                         const uint32_t b = __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu);
                         mx = __vmaxu2(mx, __vmaxu2(a, b));
                     }
                 }
                 mx = __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
-                if (lane == 0) sRed[(g & 1) * 2 + (warp & 1)] = mx;
-                mbar_arrive(v_max);
-                if (!mbar_wait_all(v_max, g & 1, abort_flag)) return false;
-                mx = max(sRed[(g & 1) * 2], sRed[(g & 1) * 2 + 1]);
+                int bnext = 0;  // b of the tile before, then of this one
+                if (g > 0) {
+                    if (!mbar_wait_all(&b_set[(g - 1) & 3], ((g - 1) >> 2) & 1, abort_flag)) return false;
+                    bnext = sB[(g - 1) & 7];
+                }
                 const bool finite = mx < 0x7F80u;
                 const int b = (int)(mx >> 7) - 127 - 12;
                 const bool changed = g == 0 || !finite || (mx != 0 && (b > bnext + 2 || b < bnext - 6));
                 if (changed) bnext = finite ? min(max(b, -100), 114) : 114;  // (not finite: S is not, either)
-                if (t == 0) {
+                if (lane == 0) {
                     sScale[g & 7] = changed;
                     sB[g & 7] = bnext;
                 }
+                __syncwarp();
+                mbar_arrive(&b_set[g & 3]);
                 mbar_arrive(&d_full[g & 3]);
                 if (finite) {
                     const uint32_t low = (uint32_t)(112 + bnext) << 7, low2 = low | (low << 16);
 #pragma unroll 1
-                    for (int nb = 0; nb < NB; ++nb) {
-                        uint4 x[8];
+                    for (int q = 0; q < 4 * NB; ++q) {
+                        uint4 x[4];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = *(const uint4 *)(vt + (size_t)(t + 64 * (8 * nb + i)) * 16);
+                        for (int i = 0; i < 4; ++i) x[i] = *(const uint4 *)(vt + (size_t)(lane + 32 * (4 * q + i)) * 16);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
+                        for (int i = 0; i < 4; ++i) {
                             uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 u[k] = ((__vmaxu2(u[k] & 0x7FFF7FFFu, low2) - low2) << 3) | (u[k] & 0x80008000u);
-                            *(uint4 *)(vt + (size_t)(t + 64 * (8 * nb + i)) * 16) = make_uint4(u[0], u[1], u[2], u[3]);
+                            *(uint4 *)(vt + (size_t)(lane + 32 * (4 * q + i)) * 16) = make_uint4(u[0], u[1], u[2], u[3]);
                         }
                     }
                 } else {
                     const float scale = __uint_as_float((uint32_t)(127 - bnext) << 23);
-                    for (int i = 0; i < 8 * NB; ++i) {
-                        uint4 *at = (uint4 *)(vt + (size_t)(t + 64 * i) * 16);
+                    for (int i = 0; i < 16 * NB; ++i) {
+                        uint4 *at = (uint4 *)(vt + (size_t)(lane + 32 * i) * 16);
                         uint32_t u[4] = {at->x, at->y, at->z, at->w};
                         for (int k = 0; k < 4; ++k)
                             u[k] = pack_f16x2(__uint_as_float(u[k] << 16) * scale, __uint_as_float(u[k] & 0xFFFF0000u) * scale);
@@ -427,12 +428,14 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             };
             const bool keys = warp < 6;
             int flushes = 0;
-            ok = keys ? conv_k(0) && (n < 2 || conv_k(1)) : conv_v(0);
+            // V is converted two tiles ahead, each tile by one of its warps, where there are slots for it
+            constexpr int lead = NS >= 4 ? 2 : 1;
+            ok = keys ? conv_k(0) && (n < 2 || conv_k(1)) : (warp & 1) == 0 ? conv_v(0) : lead == 1 || n < 2 || conv_v(1);
             for (int g = 0; ok && g < n; ++g) {
                 if (keys)
                     ok = g + 2 >= n || conv_k(g + 2);
                 else
-                    ok = g + 1 >= n || conv_v(g + 1);
+                    ok = g + lead >= n || ((g + lead) & 1) != (warp & 1) || conv_v(g + lead);
                 if (!ok || !(ok = mbar_wait_all(&d_full[g & 3], (g >> 2) & 1, abort_flag))) break;
                 const bool take = flush_before(g);
                 if (take) {
