@@ -158,11 +158,10 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
     const int node = tid - 256;  // the threads that form J's rows
     if (node >= 0 && node < n) ptr = tree_parent(p.parents + (size_t)b * T, node);
 
-    const uint32_t idesc_p = make_idesc(128, 128, kFmtBF16, 0, 0), idesc_x = make_idesc(128, MR + D, kFmtF16, 0, 0);
-    const uint64_t dKQ = make_sdesc(smem_u32(sKQ), 16, 1024), dW = make_sdesc(smem_u32(sW), 16, 1024);
-    const uint64_t dXH = make_sdesc(smem_u32(sXH), 16, 1024), dXL = make_sdesc(smem_u32(sXL), 16, 1024);
-    const uint64_t dXL1 = make_sdesc(smem_u32(sXL1), 16, 1024);
+    // (descriptors are formed where they are used: 64 registers a thread leave no room to keep them)
     auto logits = [&](int h, uint32_t col) {  // warp 0
+        constexpr uint32_t idesc_p = make_idesc(128, 128, kFmtBF16, 0, 0);
+        const uint64_t dKQ = make_sdesc(smem_u32(sKQ), 16, 1024), dW = make_sdesc(smem_u32(sW), 16, 1024);
         for (int nb = 0; nb < NB; ++nb) {
             const uint64_t w = dW + (h * NB + nb) * (C::BLK / 16);
             mma_ss_x4_w(tmem + col + C::T_K, dKQ + nb * (C::BLK / 16), w, idesc_p, nb > 0, 2, 2);
@@ -264,16 +263,22 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
 
         // row maxima of P + sgn X over this thread's columns of a half
         auto row_max = [&](uint32_t col, int h, float sgn) {
-            float mx = -INFINITY, v[32];
+            float mx = -INFINITY;
             const int f0 = 128 * h + 32 * cg;
             if (f0 >= m) return mx;
-            tmem_ld32(tL + col + 32 * cg, v);
+#pragma unroll 1
+            for (int q = 0; q < 32; q += 16) {
+                float v[16];
+                tmem_ld16(tL + col + 32 * cg + q, v);
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-                const float4 x = *(const float4 *)(sX + f0 + e);
-                const float t0 = fmaf(v[e], kLog2e, sgn * x.x), t1 = fmaf(v[e + 1], kLog2e, sgn * x.y);
-                const float t2 = fmaf(v[e + 2], kLog2e, sgn * x.z), t3 = fmaf(v[e + 3], kLog2e, sgn * x.w);
-                mx = fmax3(mx, fmaxf(t0, t1), fmaxf(t2, t3));
+                for (int e = 0; e < 16; e += 4) {
+                    const float4 x = *(const float4 *)(sX + f0 + q + e);
+                    float t[4];
+                    ffma2(v[e], v[e + 1], sgn * kLog2e, sgn * kLog2e, x.x, x.y, t[0], t[1]);
+                    ffma2(v[e + 2], v[e + 3], sgn * kLog2e, sgn * kLog2e, x.z, x.w, t[2], t[3]);
+#pragma unroll
+                    for (int k = 0; k < 4; k += 2) mx = fmax3(mx, sgn * t[k], sgn * t[k + 1]);
+                }
             }
             return mx;
         };
@@ -305,17 +310,19 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
                 for (int h = 0; h < nh; ++h) {
                     const int f0 = 128 * h + 32 * cg;
                     if (f0 >= m) break;
-                    float v[32];
-                    tmem_ld32(tL + h * C::T_H + C::T_K + 32 * cg, v);
-                    float mine = -INFINITY;
+#pragma unroll 1
+                    for (int q = 0; q < 32; q += 16) {
+                        float v[16], mine = -INFINITY;
+                        tmem_ld16(tL + h * C::T_H + C::T_K + 32 * cg + q, v);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        float u = fmaf(v[e], kLog2e, eN);
-                        if (!(row < n && fabsf(u) < INFINITY)) u = -INFINITY;
-                        u = from_order_bits(__reduce_max_sync(0xffffffffu, order_bits(u)));
-                        if (e == lane) mine = u;
+                        for (int e = 0; e < 16; ++e) {
+                            float u = fmaf(v[e], kLog2e, eN);
+                            if (!(row < n && fabsf(u) < INFINITY)) u = -INFINITY;
+                            u = from_order_bits(__reduce_max_sync(0xffffffffu, order_bits(u)));
+                            if (e == lane) mine = u;
+                        }
+                        if (lane < 16) sE[(warp & 3) * 256 + f0 + q + lane] = mine;
                     }
-                    sE[(warp & 3) * 256 + f0 + lane] = mine;
                 }
             }
             __syncthreads();
@@ -336,34 +343,34 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
         }
         if (is_key && cg == 0) sGe[row] = row < n ? ex2_approx(g2 + eN - 30.f) : 0.f;
 
-        float den_s = 0.f, sum_a = 0.f, sum_b = 0.f;  // 2^15 y_i, sum_r a_jr and b_ir, of this thread's features
+        float den_s[2] = {0.f, 0.f}, sum_a[2] = {0.f, 0.f}, sum_q[2] = {0.f, 0.f};  // 2^15 y_i, sum_r a_jr and b_ir, of this thread's features
+        float(&sum_b)[2] = STACK ? sum_a : sum_q;  // (a thread of a stacked tile has a key or a query)
         const float up = exp2f(-shift);
         // 16 features from TMEM: 2^(15 + P + sgn X - max) as hi + lo
-        auto split = [&](uint32_t col, int f, float sgn, float c, uint32_t(&hi)[8], uint32_t(&lo)[8], float &sum, bool state) {
+        auto split = [&](uint32_t col, int f, float sgn, float c, uint32_t(&hi)[8], uint32_t(&lo)[8], float(&sum)[2], bool state) {
             float v[16];
             tmem_ld16(tL + col, v);
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
                 const float4 x4 = *(const float4 *)(sX + f + e);
                 const float x[4] = {x4.x, x4.y, x4.z, x4.w};
-                float y[4], yh[4];
+                float4 s4 = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (state) s4 = *(const float4 *)(sZ + f + e);
+                const float s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    y[k] = ex2_approx(fmaf(v[e + k], kLog2e, sgn * x[k]) + c);
-                    yh[k] = tf32_trunc(y[k]);
-                    sum += y[k];
+                for (int k = 0; k < 4; k += 2) {
+                    float y0, y1, l0, l1;
+                    ffma2(v[e + k], v[e + k + 1], sgn * kLog2e, sgn * kLog2e, x[k], x[k + 1], y0, y1);
+                    ffma2(y0, y1, sgn, sgn, c, c, y0, y1);
+                    y0 = ex2_approx(y0);
+                    y1 = ex2_approx(y1);
+                    const float h0 = tf32_trunc(y0), h1 = tf32_trunc(y1);
+                    ffma2(y0, y1, 1.f, 1.f, sum[0], sum[1], sum[0], sum[1]);
+                    if (state) ffma2(y0, y1, s[k], s[k + 1], den_s[0], den_s[1], den_s[0], den_s[1]);
+                    ffma2(h0, h1, -1.f, -1.f, y0, y1, l0, l1);
+                    hi[(e + k) >> 1] = pack_f16x2(h0, h1);
+                    lo[(e + k) >> 1] = pack_f16x2(l0, l1);
                 }
-                if (state) {
-                    const float4 s4 = *(const float4 *)(sZ + f + e);
-                    den_s = fmaf(y[0], s4.x, den_s);
-                    den_s = fmaf(y[1], s4.y, den_s);
-                    den_s = fmaf(y[2], s4.z, den_s);
-                    den_s = fmaf(y[3], s4.w, den_s);
-                }
-                hi[e >> 1] = pack_f16x2(yh[0], yh[1]);
-                hi[(e >> 1) + 1] = pack_f16x2(yh[2], yh[3]);
-                lo[e >> 1] = pack_f16x2(y[0] - yh[0], y[1] - yh[1]);
-                lo[(e >> 1) + 1] = pack_f16x2(y[2] - yh[2], y[3] - yh[3]);
             }
         };
         for (int c0 = 0; c0 < nch; c0 += NSB) {  // steps of 64 NSB features
@@ -435,6 +442,9 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
             const bool next_half = (c1 & 1) == 0 && c1 < nch;
             if (warp == 0) {
                 // K-steps of 16 features: hi hi + hi lo + lo hi
+                constexpr uint32_t idesc_x = make_idesc(128, MR + D, kFmtF16, 0, 0);
+                const uint64_t dXH = make_sdesc(smem_u32(sXH), 16, 1024), dXL = make_sdesc(smem_u32(sXL), 16, 1024);
+                const uint64_t dXL1 = make_sdesc(smem_u32(sXL1), 16, 1024);
                 for (int k = 4 * c0; k < min(m, 64 * c1) / 16; ++k) {
                     const int s = (k >> 2) % NSB;
                     const uint32_t bq = tmem + C::T_Q + 16 * (k & 7);
@@ -443,18 +453,28 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
                     mma_f16_ts_w(tmem + C::T_A, bq, xl, idesc_x, 1u);
                     mma_f16_ts_w(tmem + C::T_A, bq + 8, xh, idesc_x, 1u);
                 }
-                if (next_half) logits(h + 1, 0);  // over this half's b, after the MMAs that read it
                 mma_commit_w(mma_done);
             }
             ++nc;
             if (!wait(mma_done, nm++ & 1)) break;
             tc_fence_after();
+            if (next_half) {  // over this half's b: the MMAs that read it are done
+                if (warp == 0) {
+                    logits(h + 1, 0);
+                    mma_commit_w(mma_done);
+                }
+                ++nc;
+            }
             while (ns < min(nch, c1 + NSB)) load_state();
-            if (next_half) load_values();
+            if (next_half) {
+                if (!wait(mma_done, nm++ & 1)) break;
+                tc_fence_after();
+                load_values();
+            }
         }
         if (!ok) break;
-        if (is_key) sSum[cg * 128 + row] = sum_a;
-        if (is_query) sSum[(4 + cg) * 128 + row] = sum_b;
+        if (is_key) sSum[cg * 128 + row] = sum_a[0] + sum_a[1];
+        if (is_query) sSum[(4 + cg) * 128 + row] = sum_b[0] + sum_b[1];
 
         // values: rows past the tree are not the tree's; non-finite ones must not meet a zero weight
         if (!wait(v_full, 0)) break;
@@ -477,7 +497,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
         if (is_query) {
             constexpr int KT = MR / 4;  // keys a thread takes
             const float sb = (sSum[512 + row] + sSum[640 + row]) + (sSum[768 + row] + sSum[896 + row]);
-            float den = has_state ? den_s * 0x1p-15f : 0.f, err = 0.f;
+            float den = has_state ? (den_s[0] + den_s[1]) * 0x1p-15f : 0.f, err = 0.f;
             const int j0 = KT * cg;
             const uint32_t seen = sAnc[row * (MR / 32) + (j0 >> 5)] >> (j0 & 31);
 #pragma unroll
