@@ -103,34 +103,24 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
     if (n == 0) return;
     const int nh = m > 128 ? 2 : 1, nch = (m + 63) / 64;
 
-    if (tid == 0) {
+    // chunk c of S' (64 features): its two raw blocks of 32 lie where its high and low block will
+    auto load_chunk = [&](int c) {  // one thread
+        const int s = c % NSB;
+        mbar_arrive_expect_tx(&s_full[s], D * 256);
+        tma_load_3d(sXH + s * C::XB + MR * 128, &mapS, &s_full[s], 64 * c, 0, bh);
+        tma_load_3d((s == 0 ? sXL : sXL1) + MR * 128, &mapS, &s_full[s], 64 * c + 32, 0, bh);
+    };
+    int ns = min(C::OVER ? 1 : NSB, nch);  // chunks asked for
+    auto load_state = [&]() {
+        if (warp == 0 && elect_one()) load_chunk(ns);
+        __syncwarp();
+        ++ns;
+    };
+    if (tid == 0) {  // barriers and the first copies, while another warp asks for TMEM
         for (int i = 0; i < 6; ++i) mbar_init(&bars[i], 1);
         *abort_flag = 0;
         sFlag[0] = 0;
         fence_barrier_init();
-    }
-    if (warp == 0) {
-        tmem_alloc(tmem_slot, C::COLS);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-
-    // chunk c of S' (64 features): its two raw blocks of 32 lie where its high and low block will
-    int ns = 0;  // chunks asked for
-    auto load_state = [&]() {
-        if (warp == 0 && elect_one()) {
-            const int s = ns % NSB;
-            mbar_arrive_expect_tx(&s_full[s], D * 256);
-            tma_load_3d(sXH + s * C::XB + MR * 128, &mapS, &s_full[s], 64 * ns, 0, bh);
-            tma_load_3d((s == 0 ? sXL : sXL1) + MR * 128, &mapS, &s_full[s], 64 * ns + 32, 0, bh);
-        }
-        __syncwarp();
-        ++ns;
-    };
-    if (warp == 0 && elect_one()) {
         mbar_arrive_expect_tx(kq_full, C::KQ);
         for (int nb = 0; nb < NB; ++nb) {
             tma_load_3d(sKQ + nb * C::BLK, &mapK, kq_full, 64 * nb, 0, bh);
@@ -139,24 +129,27 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
         mbar_arrive_expect_tx(w_full, nh * NB * C::BLK);
         for (int h = 0; h < nh; ++h)
             for (int nb = 0; nb < NB; ++nb) tma_load_2d(sW + (h * NB + nb) * C::BLK, &mapW, w_full, 64 * nb, 128 * h);
+        for (int c = 0; c < ns; ++c) load_chunk(c);
     }
-    __syncwarp();
-    while (ns < min(C::OVER ? 1 : NSB, nch)) load_state();
-
-    // the state's scales
-    bool empty = false, some = false;
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, C::COLS);
+        tmem_relinquish();
+    }
+    // the state's scales, asked for here, used under the logits
+    float z = 0.f, Dr = 0.f;
     if (tid < m) {
         const float *zp = p.state + (size_t)bh * ((size_t)D * m + 2 * m) + (size_t)D * m;
-        const float z = zp[tid], Dr = zp[m + tid];
-        some = z > 0.f;
-        empty = !some;
-        sX[tid] = some ? (Dr + logf(z)) * kLog2e : -INFINITY;
-        sZ[tid] = some ? 1.f : 0.f;
-        sFac[tid] = some ? 1.f / z : 0.f;
+        z = zp[tid];
+        Dr = zp[m + tid];
     }
     int ptr = -1;
     const int node = tid - 256;  // the threads that form J's rows
     if (node >= 0 && node < n) ptr = tree_parent(p.parents + (size_t)b * T, node);
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
 
     // (descriptors are formed where they are used: 64 registers a thread leave no room to keep them)
     auto logits = [&](int h, uint32_t col) {  // warp 0
@@ -194,7 +187,6 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
     };
 
     do {
-        const bool any_empty = __syncthreads_or(empty), has_state = __syncthreads_or(some);
         if (!wait(kq_full, 0) || !wait(w_full, 0)) break;
         if (warp == 0) {
             for (int h = 0; h < nh; ++h) logits(h, h * C::T_H);
@@ -226,6 +218,13 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
                 for (int w = 0; w < NW; ++w) sAnc[node * NW + w] = anc[w];
             }
         }
+        const bool some = z > 0.f;
+        if (tid < m) {
+            sX[tid] = some ? (Dr + logf(z)) * kLog2e : -INFINITY;
+            sZ[tid] = some ? 1.f : 0.f;
+            sFac[tid] = some ? 1.f / z : 0.f;
+        }
+        const bool any_empty = __syncthreads_or(tid < m && !some), has_state = __syncthreads_or(tid < m && some);
         // the size of S'/z', from its first 64 features
         if (!wait(&s_full[0], 0)) break;
         {
@@ -603,7 +602,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, C::COLS);
     }
