@@ -1,24 +1,24 @@
 // favor_decode_tree on tensor cores: bf16 trees of enough nodes to fill tiles, one CTA per head.
 //
 // With P = w_r.x the projections and X_r a scale per feature (below), in log2 units:
-//   b_ir = 2^(P_ir + X_r - f_i),   f_i = max_r (P_ir + X_r)           query rows
-//   a_jr = 2^(P_jr - X_r - g_j),   g_j = max_r (P_jr - X_r)           key rows
-//   A_ij = sum_r b_ir a_jr,   Y_ic = sum_r b_ir s_r S'_r[c] / z'_r,   y_i = sum_r b_ir s_r
+//   b_ir = 2^(P_ir + X_r - f_i),   f_i = max_r (P_ir + X_r), rounded up      query rows
+//   a_jr = 2^(P_jr - X_r - g_j),   g_j = max_r (P_jr - X_r), rounded up      key rows
+//   A_ij = sum_r b_ir a_jr,   Y_ic = sum_r b_ir s_r S'_r[c],   y_i = sum_r b_ir s_r z'_r,   s_r = 2^(D_r - X_r)
 //   G_j = g_j - |k_j|^2/2,    w_ij = 2^G_j A_ij for j in J(i), else 0
 //   out_i = [Y_i + sum_j w_ij v_j] / [y_i + sum_j w_ij].
-// X_r = D_r + log z'_r, the feature's own sum over the state, makes s_r = 1, S'_r / z'_r a weighted
-// mean of the values (of one size for all features) and y_i >= 1. Where a feature is empty or some key
-// lies far above the state (kTreeTcRaise), X_r is raised to the largest logit of the tree's keys, and
-// s_r = 2^(old X_r - X_r).
+// X_r = D_r + log2 z'_r, the feature's own sum over the state, makes s_r S'_r a weighted mean of the
+// values (of one size for all features) and y_i at least about 1. Where a feature is empty or some key
+// lies far above the state (kTreeTcRaise), X_r is raised to the largest logit of the tree's keys. X, f
+// and g are whole numbers, so that the exponents of a row's large terms are small and rounded once.
 //
-// Precision: a, b and S'/z' enter the MMAs as hi + lo, two fp16 values (22 bits), products hi hi,
+// Precision: a, b and s S' enter the MMAs as hi + lo, two fp16 values (22 bits), products hi hi,
 // hi lo, lo hi; a and b are scaled by 2^15, so that a term 2^-18 below its maximum keeps all 22 bits
-// and fp16's smallest step is an error of at most 2^-40 of the maximum. S'/z' is scaled by its first
+// and fp16's smallest step is an error of at most 2^-40 of the maximum. s S' is scaled by its first
 // 64 features' largest magnitude to about 1. Weights of values are three bf16 parts against the bf16
 // values. The steps' error in a row's denominator is at most
 //   2^-40 sum_{j in J(i)} 2^G_j (sum_r a_jr + sum_r b_ir);
 // a row where that bound exceeds 2^-14 of the denominator (its own terms lie far below the scales of
-// other rows'), and every row of a head with a non-finite value or S'/z' beyond fp16's range, is
+// other rows'), and every row of a head with a non-finite value or s S' beyond fp16's range, is
 // computed by tree_row_exact. (A floor under the denominator instead of the bound sent one row in a
 // thousand there at d = 128 behind short contexts, and a row takes as long as a head.)
 //
@@ -83,7 +83,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
     uint8_t *sKQ = smem, *sW = smem + C::OFF_W, *sXH = smem + C::OFF_XH, *sXL = smem + C::OFF_XL;
     uint8_t *sXL1 = C::OVER ? sW : sXL + C::XB;
     uint8_t *sV = sKQ;                                    // the values take the keys' place
-    float *sX = (float *)(smem + C::OFF_F), *sZ = sX + 256, *sFac = sZ + 256;  // X_r, s_r, s_r / z'_r
+    float *sX = (float *)(smem + C::OFF_F), *sZ = sX + 256, *sFac = sZ + 256;  // X_r, s_r z'_r, s_r
     float *sMx = sFac + 256;                              // [keys, queries][4 column groups][128] maxima
     float *sDen = sMx, *sErr = sMx + 4 * 128;             // then [4][128] parts of denominators and their errors
     float *sSum = sMx + 8 * 128;                          // [keys, queries][4][128] sums of a and b
@@ -175,7 +175,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
     const bool is_key = !STACK || (warp & 3) < 2, is_query = !STACK || (warp & 3) >= 2;
     const uint32_t tL = tmem + (((uint32_t)(warp & 3) * 32u) << 16);
     float eN = 0.f;     // -|k|^2/2 of this thread's key, log2 units
-    float shift = 0.f;  // S'/z' enters as 2^-shift of itself
+    float shift = 0.f;  // s S' enters as 2^-shift of itself
     bool v_asked = false;
     auto load_values = [&]() {
         if (warp == 0 && elect_one()) {
@@ -220,12 +220,14 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
         }
         const bool some = z > 0.f;
         if (tid < m) {
-            sX[tid] = some ? (Dr + logf(z)) * kLog2e : -INFINITY;
-            sZ[tid] = some ? 1.f : 0.f;
-            sFac[tid] = some ? 1.f / z : 0.f;
+            const double D2 = (double)Dr * 1.4426950408889634074;
+            const float X = rintf((float)D2 + log2f(z)), s = some ? exp2f((float)(D2 - (double)X)) : 0.f;
+            sX[tid] = some ? X : -INFINITY;
+            sZ[tid] = some ? s * z : 0.f;
+            sFac[tid] = s;
         }
         const bool any_empty = __syncthreads_or(tid < m && !some), has_state = __syncthreads_or(tid < m && some);
-        // the size of S'/z', from its first 64 features
+        // the size of s S', from its first 64 features
         if (!wait(&s_full[0], 0)) break;
         {
             float mx = 0.f;
@@ -256,7 +258,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
             float mx = sRed[0];
 #pragma unroll
             for (int w = 1; w < min(D / 8, kTreeTcThreads / 32); ++w) mx = fmaxf(mx, sRed[w]);
-            // its exponent (|shift| <= 110 keeps 2^-shift / z' a normal number for any z' in use)
+            // its exponent (|shift| <= 110 keeps 2^-shift s_r a normal number)
             shift = mx > 0.f ? (float)min(max((int)(__float_as_uint(mx) >> 23) - 127, -110), 110) : 0.f;
         }
 
@@ -294,8 +296,8 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
                 sMx[(4 + cg) * 128 + row] = x;
             }
             __syncthreads();
-            if (is_key) g2 = fmaxf(fmaxf(sMx[row], sMx[128 + row]), fmaxf(sMx[256 + row], sMx[384 + row]));
-            if (is_query) f2 = fmaxf(fmaxf(sMx[512 + row], sMx[640 + row]), fmaxf(sMx[768 + row], sMx[896 + row]));
+            if (is_key) g2 = ceilf(fmaxf(fmaxf(sMx[row], sMx[128 + row]), fmaxf(sMx[256 + row], sMx[384 + row])));
+            if (is_query) f2 = ceilf(fmaxf(fmaxf(sMx[512 + row], sMx[640 + row]), fmaxf(sMx[768 + row], sMx[896 + row])));
         };
         bool raise = any_empty;
         if (!raise) {
@@ -330,7 +332,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
 #pragma unroll
                 for (int w = 1; w < MR / 32; ++w) E = fmaxf(E, sE[w * 256 + tid]);
                 const float old = sX[tid];
-                float x = fmaxf(old, E);
+                float x = fmaxf(old, rintf(E));
                 if (!(fabsf(x) < INFINITY)) x = 0.f;
                 const float s = exp2f(old - x);
                 sX[tid] = x;
@@ -340,7 +342,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
             __syncthreads();
             maxima();
         }
-        if (is_key && cg == 0) sGe[row] = row < n ? ex2_approx(g2 + eN - 30.f) : 0.f;
+        if (is_key && cg == 0) sGe[row] = row < n ? exp2f(g2 + eN) * 0x1p-30f : 0.f;
 
         float den_s[2] = {0.f, 0.f}, sum_a[2] = {0.f, 0.f}, sum_q[2] = {0.f, 0.f};  // 2^15 y_i, sum_r a_jr and b_ir, of this thread's features
         float(&sum_b)[2] = STACK ? sum_a : sum_q;  // (a thread of a stacked tile has a key or a query)
@@ -359,10 +361,11 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
 #pragma unroll
                 for (int k = 0; k < 4; k += 2) {
                     float y0, y1, l0, l1;
-                    ffma2(v[e + k], v[e + k + 1], sgn * kLog2e, sgn * kLog2e, x[k], x[k + 1], y0, y1);
-                    ffma2(y0, y1, sgn, sgn, c, c, y0, y1);
+                    ffma2(x[k], x[k + 1], sgn, sgn, c, c, y0, y1);  // whole numbers: exact
+                    ffma2(v[e + k], v[e + k + 1], kLog2e, kLog2e, y0, y1, y0, y1);
                     y0 = ex2_approx(y0);
                     y1 = ex2_approx(y1);
+                    ffma2(y0, y1, 0x1p15f, 0x1p15f, 0.f, 0.f, y0, y1);
                     const float h0 = tf32_trunc(y0), h1 = tf32_trunc(y1);
                     ffma2(y0, y1, 1.f, 1.f, sum[0], sum[1], sum[0], sum[1]);
                     if (state) ffma2(y0, y1, s[k], s[k + 1], den_s[0], den_s[1], den_s[0], den_s[1]);
@@ -382,7 +385,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
                 if (f >= m) break;
                 uint32_t hi[8], lo[8];
                 if (is_key) {
-                    split(C::T_K + col, f, -1.f, 15.f - g2, hi, lo, sum_a, false);
+                    split(C::T_K + col, f, -1.f, -g2, hi, lo, sum_a, false);
                     uint8_t *xh = sXH + blk * C::XB, *xl = blk == 0 ? sXL : sXL1;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -392,13 +395,13 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
                     }
                 }
                 if (is_query) {
-                    split(C::T_Q + col, f, 1.f, 15.f - f2, hi, lo, sum_b, true);
+                    split(C::T_Q + col, f, 1.f, -f2, hi, lo, sum_b, true);
                     tmem_st8u(tL + C::T_Q + col, hi);
                     tmem_st8u(tL + C::T_Q + col + 8, lo);
                 }
             }
             tmem_wait_st();
-            // S'/z' of the step in place: the rows of a chunk's raw blocks (32 features each) become its
+            // s S' of the step in place: the rows of a chunk's raw blocks (32 features each) become its
             // high and low block of 64 features
             for (int c = c0; c < c1; ++c)
                 if (!wait(&s_full[c % NSB], (c / NSB) & 1)) break;
@@ -440,18 +443,20 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
             tc_fence_after();
             const bool next_half = (c1 & 1) == 0 && c1 < nch;
             if (warp == 0) {
-                // K-steps of 16 features: hi hi + hi lo + lo hi
+                // K-steps of 16 features: hi lo and lo hi of all, then hi hi. (Each addition truncates the
+                // accumulator; the first two thirds of a first half's then truncate a small one.)
                 constexpr uint32_t idesc_x = make_idesc(128, MR + D, kFmtF16, 0, 0);
                 const uint64_t dXH = make_sdesc(smem_u32(sXH), 16, 1024), dXL = make_sdesc(smem_u32(sXL), 16, 1024);
                 const uint64_t dXL1 = make_sdesc(smem_u32(sXL1), 16, 1024);
-                for (int k = 4 * c0; k < min(m, 64 * c1) / 16; ++k) {
-                    const int s = (k >> 2) % NSB;
-                    const uint32_t bq = tmem + C::T_Q + 16 * (k & 7);
-                    const uint64_t xh = dXH + s * (C::XB / 16) + 2 * (k & 3), xl = (s == 0 ? dXL : dXL1) + 2 * (k & 3);
-                    mma_f16_ts_w(tmem + C::T_A, bq, xh, idesc_x, k > 0);
-                    mma_f16_ts_w(tmem + C::T_A, bq, xl, idesc_x, 1u);
-                    mma_f16_ts_w(tmem + C::T_A, bq + 8, xh, idesc_x, 1u);
-                }
+                const int k0 = 4 * c0, k1 = min(m, 64 * c1) / 16;
+#pragma unroll 1
+                for (int i = 0; i < 3; ++i)
+#pragma unroll 1
+                    for (int k = k0; k < k1; ++k) {
+                        const int s = (k >> 2) % NSB;
+                        const uint64_t x = (i != 0 ? dXH : s == 0 ? dXL : dXL1) + (i != 0 ? s * (C::XB / 16) : 0) + 2 * (k & 3);
+                        mma_f16_ts_w(tmem + C::T_A, tmem + C::T_Q + 16 * (k & 7) + (i == 1 ? 8 : 0), x, idesc_x, k + i > 0);
+                    }
                 mma_commit_w(mma_done);
             }
             ++nc;
@@ -540,9 +545,9 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
         if (warp == 0) {
             const uint32_t idesc = make_idesc(128, D, kFmtBF16, 0, 1);
             const uint64_t dV = make_sdesc(smem_u32(sV), MR * 128, 1024);
-            for (int k = 0; k < (n + 15) / 16; ++k)
-                for (int t = 0; t < 3; ++t)
-                    mma_f16_ts_w(tmem + C::T_O, tmem + t * (MR / 2) + 8 * k, dV + k * (16 * 128 / 16), idesc, k + t > 0);
+            for (int t = 2; t >= 0; --t)  // the small parts first, as above
+                for (int k = 0; k < (n + 15) / 16; ++k)
+                    mma_f16_ts_w(tmem + C::T_O, tmem + t * (MR / 2) + 8 * k, dV + k * (16 * 128 / 16), idesc, t < 2 || k > 0);
             mma_commit_w(mma_done);
         }
         ++nc;
@@ -561,7 +566,11 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
         float *sOut = (float *)sW;
         if (is_query) {
             if (cg == 0) sPtr[row] = good && sFlag[0] == 0;
-            const float fy = ex2_approx(shift - 15.f);
+            // Y's accumulator was truncated by each addition at its full size, 1.8e-8 of it a time on average
+            // (measured against 64 bits at m = 32, 128, 256: 1.9e-7, 3.3e-7, 7.3e-7 low in all), while y_i is
+            // summed with rounding; what is expected to be missing is added back.
+            const float lost = 1.8e-8f * (float)(min(m, 64 * NSB) / 16 + 3 * max(m - 64 * NSB, 0) / 16);
+            const float fy = ex2_approx(shift - 15.f) * (1.f + lost);
             constexpr int CT = D / 4;  // columns a thread takes
 #pragma unroll
             for (int q = 0; q < CT; q += 16) {
