@@ -1129,12 +1129,11 @@ bool tree_on_tiles(const favor_shape *s) {
     return s->L > kRowsTile || (long long)s->B * s->H * (s->d / kRowsCols) > num_sms();
 }
 
-// How favor_decode_extend takes n_tok tokens a head: on tensor cores (bf16 in order) or CUDA cores,
+// How favor_decode_extend takes n_tok tokens a head: on tiles (bf16 in order) or warp MMAs,
 // and the runs each head is cut into.
-//   CUDA cores: up to kExtWhole tokens (an accepted path, a short prompt) one CTA a head updates the
-//   state in place; more are cut so that about four CTAs an SM are in flight.
+//   Warp MMAs: up to kExtPath tokens (an accepted path) one CTA a head updates the state in place; more
+//   are cut so that the CTAs fill the SMs once (two to an SM up to 128 features).
 //   Tensor cores: as many runs of whole tiles as fill two CTAs an SM once (d = 128: kExtFlush tiles at most).
-constexpr int kExtWhole = 32;
 constexpr int kExtTcMin = 64;
 struct ExtendPlan {
     bool tc;
@@ -1150,10 +1149,10 @@ ExtendPlan extend_plan(const favor_shape *s, int n_tok, bool indexed) {
         if (s->d == 128) per = std::min<long long>(per, kExtFlush);
         return {true, (int)((nt + per - 1) / per), (int)(per * kExtTile)};
     }
-    if (n_tok <= kExtWhole) return {false, 1, n_tok};
-    const long long ctas = 4ll * num_sms();
-    long long per = std::max<long long>(kExtWhole, (BH * n_tok + ctas - 1) / ctas);
-    per = std::min<long long>((per + kExtTok - 1) / kExtTok * kExtTok, n_tok);
+    if (n_tok <= kExtPath) return {false, 1, n_tok};
+    const long long ctas = (s->m <= 128 ? 2ll : 1ll) * num_sms(), cols = s->d / kExtRowCols;
+    long long per = std::max<long long>(2 * kExtBlk, (BH * cols * n_tok + ctas - 1) / ctas);
+    per = std::min<long long>((per + kExtBlk - 1) / kExtBlk * kExtBlk, n_tok);
     return {false, (int)((n_tok + per - 1) / per), (int)per};
 }
 
@@ -1184,7 +1183,8 @@ extern "C" favor_status favor_decode_tree(const favor_shape *s, const void *q, c
 extern "C" size_t favor_decode_extend_workspace_size(const favor_shape *s, int n_index) {
     if (!shape_ok(s) || n_index < 0 || !decode_supported(s)) return 0;
     const ExtendPlan pl = extend_plan(s, n_index > 0 ? n_index : s->L, n_index > 0);
-    if (pl.n_split == 1 && !(pl.tc && s->d == 128)) return 256;  // (on tiles, d = 128 sums in a partial state)
+    // (at d = 128 two CTAs of a head add their columns through a partial state, one run or not)
+    if (pl.n_split == 1 && (s->d == 64 || (!pl.tc && pl.tok_per_split <= kExtPath))) return 256;
     return align256((size_t)s->B * s->H * pl.n_split * ((size_t)s->d * s->m + 2 * s->m) * 4);
 }
 

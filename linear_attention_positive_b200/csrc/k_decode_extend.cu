@@ -38,99 +38,286 @@ __device__ __forceinline__ int extend_token(const ExtendParams &p, int b, int t)
     return j;
 }
 
-// ------------------------------------------------------------------------------- CUDA-core kernel
+// ------------------------------------------------------------------------------- rows on warp MMAs
 //
-// One CTA per (head, run of tokens), one thread per feature with the feature's row of S' in
-// registers; eight tokens at a time, so that W's row is streamed once per eight. With one run per
-// head the state is read and written in place: for the few tokens of an accepted path that traffic,
-// (m d + 2 m) * 8 bytes a head, is the bound. Longer inputs are split into runs whose partial states
-// k_extend_combine adds.
+// fp32 tokens, and bf16 ones by index or too few for tiles. One CTA per (run of tokens, head, 64 value
+// columns), a warp per 32 features, W in shared memory, 16 tokens at a time, double-buffered. All in
+// registers: P's accumulator fragments (features x tokens) become phi and are the next MMA's A operand as
+// they stand, with tokens 2t, 2t + 1 in the places of K = t, t + 4 on both sides. Products are tf32 with
+// both operands hi + lo (three MMAs, 2^-22; bf16 operands are exact in one part); the S accumulators are
+// added to fp32 registers every 64 tokens, since the tensor core truncates as it accumulates.
+// Bound: instruction issue, about 900 a warp and block at d = 64.
 
-constexpr int kExtTok = 8;
+constexpr int kExtBlk = 16;
+constexpr int kExtRowCols = 64;
 
-template <int D>
-__global__ void __launch_bounds__(256) k_decode_extend_rows(ExtendParams p) {
-    __shared__ __align__(16) float sK[kExtTok * D], sV[kExtTok * D];
-    __shared__ float sN[kExtTok];
-    __shared__ int sT[kExtTok];
-    const int bh = blockIdx.y, b = bh / p.H, split = blockIdx.x, m = p.m, r = threadIdx.x;
-    const int warp = r >> 5, lane = r & 31, nw = m >> 5;
+template <int D, bool BF16>
+struct ExtRows {
+    static constexpr int ES = BF16 ? 2 : 4;
+    // row strides in bytes: 64 mod 128 for 16-byte fragments, 16 mod 64 apart by two rows for values
+    static constexpr int LDW = D * ES + 64, LDV = kExtRowCols * ES + 16;
+    static constexpr size_t KV = (size_t)kExtBlk * (LDW + LDV);
+    static size_t bytes(int m) { return (size_t)m * LDW + 2 * KV + 2 * kExtBlk * 4; }
+};
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256, 1) k_decode_extend_rows(ExtendParams p) {
+    using C = ExtRows<D, BF16>;
+    constexpr int ES = C::ES, NT = kExtRowCols / 8;
+    extern __shared__ __align__(16) uint8_t sm8[];
+    const int split = blockIdx.x, bh = blockIdx.y, b = bh / p.H, v0 = blockIdx.z * kExtRowCols, m = p.m;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3, f0 = 32 * warp;
     const int n = extend_count(p, b);
-    const bool whole = p.n_split == 1;
     if (n == 0) return;  // the state stays as it is
-    const size_t len = (size_t)D * m + 2 * m;
-    float *S = whole ? p.state + (size_t)bh * len : p.part + ((size_t)bh * p.n_split + split) * len;
-    float *z = S + (size_t)D * m, *Dl = z + m;
     const int t0 = split * p.tok_per_split, t1 = min(n, t0 + p.tok_per_split);
     if (t0 >= t1) return;  // an empty run
-    float s[D], zr = 0.f, Dr = -INFINITY;
-    if (split == 0) {  // the first run starts from the carried state
-        const float *S0 = p.state + (size_t)bh * len;
-        zr = S0[(size_t)D * m + r];
-        if (zr != 0.f) Dr = S0[(size_t)D * m + m + r];
-#pragma unroll
-        for (int c = 0; c < D; ++c) s[c] = zr != 0.f ? S0[(size_t)c * m + r] : 0.f;
-    } else {
-#pragma unroll
-        for (int c = 0; c < D; ++c) s[c] = 0.f;
-    }
+    const bool whole = p.n_split == 1 && D == 64;  // (two CTAs of a head must not meet in its state)
+    const size_t len = (size_t)D * m + 2 * m;
+    uint8_t *sW = sm8, *sTok = sW + (size_t)m * C::LDW;
+    int *sUse = (int *)(sTok + 2 * C::KV);  // [2][16]: a token that is added
     const size_t row0 = (size_t)bh * p.L;
-    for (int t = t0; t < t1; t += kExtTok) {
-        const int nt = min(kExtTok, t1 - t);
+
+    for (int i = tid; i < m * (D * ES / 16); i += blockDim.x) {
+        const int r = i / (D * ES / 16), c = i % (D * ES / 16);
+        cp_async16(sW + (size_t)r * C::LDW + 16 * c, (const char *)p.W + (size_t)r * D * ES + 16 * c);
+    }
+    auto fetch = [&](int blk) {  // tokens of block blk into its buffer
+        uint8_t *kb = sTok + (blk & 1) * C::KV, *vb = kb + kExtBlk * C::LDW;
+        constexpr int KC = D * ES / 16, VC = kExtRowCols * ES / 16;
+        for (int i = tid; i < kExtBlk * (KC + VC); i += blockDim.x) {
+            const int j = i / (KC + VC), c = i % (KC + VC), tok = t0 + blk * kExtBlk + j;
+            const int at = tok < t1 ? extend_token(p, b, tok) : -1;
+            uint8_t *dst = c < KC ? kb + j * C::LDW + 16 * c : vb + j * C::LDV + 16 * (c - KC);
+            if (at >= 0)
+                cp_async16(dst, c < KC ? (const char *)p.k + (row0 + at) * D * ES + 16 * c
+                                       : (const char *)p.v + ((row0 + at) * D + v0) * ES + 16 * (c - KC));
+            else
+                *(uint4 *)dst = make_uint4(0u, 0u, 0u, 0u);
+            if (c == 0) sUse[(blk & 1) * kExtBlk + j] = at >= 0;
+        }
+        cp_async_commit();
+    };
+    const int nblk = (t1 - t0 - 1) / kExtBlk + 1;
+    fetch(0);
+
+    float S[2][NT][4], acc[2][NT][4], z[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+    float Dr[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int c = 0; c < NT; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[a][c][e] = acc[a][c][e] = 0.f;
+
+    for (int blk = 0; blk < nblk; ++blk) {
+        cp_async_wait_all();
         __syncthreads();
-        if (r < kExtTok) sT[r] = r < nt ? extend_token(p, b, t + r) : -1;
-        __syncthreads();
-        for (int i = r; i < kExtTok * D; i += m) {
-            const int j = sT[i / D];
-            const size_t at = (row0 + (j < 0 ? 0 : j)) * D + i % D;
-            sK[i] = j < 0 ? 0.f : ld_elem(p.k, p.bf16, at);
-            sV[i] = j < 0 ? 0.f : ld_elem(p.v, p.bf16, at);
-        }
-        __syncthreads();
-        for (int i = warp; i < kExtTok; i += nw) {
-            float x = 0.f;
-            for (int c = lane; c < D; c += 32) x = fmaf(sK[i * D + c], sK[i * D + c], x);
-            x = warp_sum(x);
-            if (lane == 0) sN[i] = 0.5f * x;
-        }
-        float u[kExtTok];
-        feature_dots<D, kExtTok>(p.W, p.bf16, r, sK, u);
-        __syncthreads();
-        float Dn = Dr;
+        if (blk + 1 < nblk) fetch(blk + 1);
+        const uint8_t *kb = sTok + (blk & 1) * C::KV, *vb = kb + kExtBlk * C::LDW;
+        // P: [32 features][16 tokens]
+        float P[2][2][4], Q[2][2][4], sq[2] = {0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < kExtTok; ++i) {
-            u[i] = sT[i] < 0 ? -INFINITY : u[i] - sN[i];
-            Dn = fmaxf(Dn, u[i]);
-        }
-        if (Dn > Dr) {
-            const float sc = zr != 0.f ? expf(Dr - Dn) : 0.f;
-            zr *= sc;
+        for (int a = 0; a < 2; ++a)
 #pragma unroll
-            for (int c = 0; c < D; ++c) s[c] *= sc;
-            Dr = Dn;
-        }
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int i = 0; i < kExtTok; ++i) {
-            u[i] = u[i] == -INFINITY ? 0.f : expf(u[i] - Dr);
-            zr += u[i];
-        }
+                for (int e = 0; e < 4; ++e) P[a][c][e] = Q[a][c][e] = 0.f;
+        const uint8_t *wr = sW + (size_t)(f0 + g) * C::LDW + 16 * t, *kr = kb + g * C::LDW + 16 * t;
+#pragma unroll 2
+        for (int j = 0; j < D * ES / 64; ++j) {
+            uint4 w[2][2], x[2];
 #pragma unroll
-        for (int c = 0; c < D; c += 4) {
+            for (int a = 0; a < 2; ++a)
 #pragma unroll
-            for (int i = 0; i < kExtTok; ++i) {
-                const float4 x = *(const float4 *)(sV + i * D + c);
-                s[c] = fmaf(u[i], x.x, s[c]);
-                s[c + 1] = fmaf(u[i], x.y, s[c + 1]);
-                s[c + 2] = fmaf(u[i], x.z, s[c + 2]);
-                s[c + 3] = fmaf(u[i], x.w, s[c + 3]);
+                for (int h = 0; h < 2; ++h) w[a][h] = *(const uint4 *)(wr + (size_t)(16 * a + 8 * h) * C::LDW + 64 * j);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) x[c] = *(const uint4 *)(kr + (size_t)8 * c * C::LDW + 64 * j);
+            if constexpr (BF16) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const uint32_t u[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float lo = __uint_as_float(u[e] << 16), hi = __uint_as_float(u[e] & 0xFFFF0000u);
+                        sq[c] = fmaf(lo, lo, sq[c]);
+                        sq[c] = fmaf(hi, hi, sq[c]);
+                    }
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) {
+                        mma_bf16_16x8x16(P[a][c], w[a][0].x, w[a][1].x, w[a][0].y, w[a][1].y, x[c].x, x[c].y);
+                        mma_bf16_16x8x16(P[a][c], w[a][0].z, w[a][1].z, w[a][0].w, w[a][1].w, x[c].z, x[c].w);
+                    }
+                }
+            } else {
+                uint32_t xh[2][4], xl[2][4];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const uint32_t u[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float f = __uint_as_float(u[e]);
+                        sq[c] = fmaf(f, f, sq[c]);
+                        tf32_split(f, xh[c][e], xl[c][e]);
+                    }
+                }
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    const uint32_t u0[4] = {w[a][0].x, w[a][0].y, w[a][0].z, w[a][0].w};
+                    const uint32_t u1[4] = {w[a][1].x, w[a][1].y, w[a][1].z, w[a][1].w};
+                    uint32_t h0[4], l0[4], h1[4], l1[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        tf32_split(__uint_as_float(u0[e]), h0[e], l0[e]);
+                        tf32_split(__uint_as_float(u1[e]), h1[e], l1[e]);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            mma_tf32_16x8x8(Q[a][c], l0[e], l1[e], l0[e + 1], l1[e + 1], xh[c][e], xh[c][e + 1]);
+                            mma_tf32_16x8x8(Q[a][c], h0[e], h1[e], h0[e + 1], h1[e + 1], xl[c][e], xl[c][e + 1]);
+                            mma_tf32_16x8x8(P[a][c], h0[e], h1[e], h0[e + 1], h1[e + 1], xh[c][e], xh[c][e + 1]);
+                        }
+                }
             }
         }
-    }
-    if (zr == 0.f && whole) return;  // no token entered this feature
+        // u = P - |k|^2/2 of tokens 8c + 2t, 8c + 2t + 1 (-inf for one that is not added)
 #pragma unroll
-    for (int c = 0; c < D; ++c) S[(size_t)c * m + r] = s[c];
-    z[r] = zr;
-    Dl[r] = Dr;
+        for (int c = 0; c < 2; ++c) {
+            sq[c] += __shfl_xor_sync(0xffffffffu, sq[c], 1);
+            sq[c] += __shfl_xor_sync(0xffffffffu, sq[c], 2);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float h = 0.5f * __shfl_sync(0xffffffffu, sq[c], 4 * (2 * t + e));
+                const bool use = sUse[(blk & 1) * kExtBlk + 8 * c + 2 * t + e] != 0;
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    P[a][c][e] = use ? P[a][c][e] + Q[a][c][e] - h : -INFINITY;
+                    P[a][c][2 + e] = use ? P[a][c][2 + e] + Q[a][c][2 + e] - h : -INFINITY;
+                }
+            }
+        }
+        // D_r, then phi (in P's place)
+        bool raise = false;
+        float Dn[2][2];
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x = fmaxf(fmaxf(P[a][0][2 * h], P[a][0][2 * h + 1]), fmaxf(P[a][1][2 * h], P[a][1][2 * h + 1]));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                Dn[a][h] = fmaxf(Dr[a][h], x);
+                raise = raise || Dn[a][h] > Dr[a][h];
+            }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float keep = Dr[a][h] == -INFINITY ? 0.f : expf(Dr[a][h] - Dn[a][h]);
+                    Dr[a][h] = Dn[a][h];
+                    z[a][h] *= keep;
+#pragma unroll
+                    for (int c = 0; c < NT; ++c)
+#pragma unroll
+                        for (int e = 2 * h; e < 2 * h + 2; ++e) {
+                            S[a][c][e] *= keep;
+                            acc[a][c][e] *= keep;
+                        }
+                }
+        }
+        uint32_t ph[2][2][4], pl[2][2][4];
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float u = P[a][c][e];
+                    const float x = u == -INFINITY ? 0.f : ex2_approx((u - Dr[a][e >> 1]) * kLog2e);
+                    z[a][e >> 1] += x;
+                    tf32_split(x, ph[a][c][e], pl[a][c][e]);
+                }
+        // acc += phi v
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int q = 0; q < NT; ++q) {
+                const uint8_t *at = vb + (size_t)(8 * c + 2 * t) * C::LDV + (8 * q + g) * ES;
+                uint32_t vh[2], vl[2] = {0u, 0u};
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if constexpr (BF16)
+                        vh[e] = (uint32_t)*(const uint16_t *)(at + e * C::LDV) << 16;
+                    else
+                        tf32_split(*(const float *)(at + e * C::LDV), vh[e], vl[e]);
+                }
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    mma_tf32_16x8x8(acc[a][q], pl[a][c][0], pl[a][c][2], pl[a][c][1], pl[a][c][3], vh[0], vh[1]);
+                    if constexpr (!BF16)
+                        mma_tf32_16x8x8(acc[a][q], ph[a][c][0], ph[a][c][2], ph[a][c][1], ph[a][c][3], vl[0], vl[1]);
+                    mma_tf32_16x8x8(acc[a][q], ph[a][c][0], ph[a][c][2], ph[a][c][1], ph[a][c][3], vh[0], vh[1]);
+                }
+            }
+        if ((blk & 3) == 3 || blk + 1 == nblk) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int c = 0; c < NT; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        S[a][c][e] += acc[a][c][e];
+                        acc[a][c][e] = 0.f;
+                    }
+        }
+    }
+    // the run's sums, joined with the carried state by the first run
+    const float *old = p.state + (size_t)bh * len;
+    float *dst = whole ? p.state + (size_t)bh * len : p.part + ((size_t)bh * p.n_split + split) * len;
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = f0 + 16 * a + 8 * h + g;
+            float zr = z[a][h], fx = 1.f, fy = 0.f, Dn = Dr[a][h];
+            zr += __shfl_xor_sync(0xffffffffu, zr, 1);
+            zr += __shfl_xor_sync(0xffffffffu, zr, 2);
+            if (split == 0) {
+                const float z_old = old[(size_t)D * m + r], D_old = old[(size_t)D * m + m + r];
+                if (z_old != 0.f) {
+                    Dn = fmaxf(D_old, Dn);
+                    fy = expf(D_old - Dn);
+                    fx = zr != 0.f ? expf(Dr[a][h] - Dn) : 0.f;
+                    zr = fmaf(z_old, fy, zr * fx);
+                }
+            }
+            float y[2 * NT];
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    y[2 * c + e] = fy != 0.f ? __ldcg(old + (size_t)(v0 + 8 * c + 2 * t + e) * m + r) : 0.f;
+            __syncwarp();  // the row's four lanes have read z' and D of the carried state
+            if (zr != 0.f || !whole) {
+#pragma unroll
+                for (int c = 0; c < NT; ++c)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        dst[(size_t)(v0 + 8 * c + 2 * t + e) * m + r] = fmaf(y[2 * c + e], fy, S[a][c][2 * h + e] * fx);
+                if (v0 == 0 && t == 0) {
+                    dst[(size_t)D * m + r] = zr;
+                    dst[(size_t)D * m + m + r] = Dn;
+                }
+            }
+        }
 }
 
 // ------------------------------------------------------------------------------- accepted paths
@@ -313,14 +500,22 @@ __global__ void __launch_bounds__(256) k_extend_combine(ExtendParams p, int d) {
     }
 }
 
+template <int D, bool BF16>
+static cudaError_t launch_extend_rows(const ExtendParams &p, cudaStream_t st) {
+    const size_t sm = ExtRows<D, BF16>::bytes(p.m);
+    const cudaError_t e = cudaFuncSetAttribute(k_decode_extend_rows<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+    if (e != cudaSuccess) return e;
+    k_decode_extend_rows<D, BF16><<<dim3(p.n_split, p.B * p.H, D / kExtRowCols), p.m, sm, st>>>(p);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_decode_extend(const ExtendParams &p, int d, cudaStream_t st) {
     const int BH = p.B * p.H;
     if (p.n_tok <= kExtPath) return d == 64 ? launch_extend_path<64>(p, st) : launch_extend_path<128>(p, st);
-    if (d == 64)
-        k_decode_extend_rows<64><<<dim3(p.n_split, BH), p.m, 0, st>>>(p);
-    else
-        k_decode_extend_rows<128><<<dim3(p.n_split, BH), p.m, 0, st>>>(p);
-    if (p.n_split > 1) k_extend_combine<<<dim3(d / kCombCols, BH), p.m, 0, st>>>(p, d);
+    const cudaError_t e = d == 64 ? (p.bf16 ? launch_extend_rows<64, true>(p, st) : launch_extend_rows<64, false>(p, st))
+                                  : (p.bf16 ? launch_extend_rows<128, true>(p, st) : launch_extend_rows<128, false>(p, st));
+    if (e != cudaSuccess) return e;
+    if (p.n_split > 1 || d != 64) k_extend_combine<<<dim3(d / kCombCols, BH), p.m, 0, st>>>(p, d);
     return cudaGetLastError();
 }
 

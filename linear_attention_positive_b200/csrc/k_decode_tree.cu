@@ -169,42 +169,6 @@ __device__ __noinline__ void tree_row_exact(const TreeParams &p, int bh, int i, 
     for (int c = 0; c < D / 32; ++c) p.out[row0 + (size_t)i * D + lane + 32 * c] = num[c] / den;
 }
 
-// acc[t] = w_r . x_t for NT tokens held in shared memory as fp32 rows.
-template <int D, int NT>
-__device__ __forceinline__ void feature_dots(const void *W, int bf16, int r, const float *sX, float (&acc)[NT]) {
-#pragma unroll
-    for (int t = 0; t < NT; ++t) acc[t] = 0.f;
-#pragma unroll 2
-    for (int c = 0; c < D; c += 8) {
-        float w[8];
-        if (bf16) {
-            const uint4 u = __ldg((const uint4 *)((const uint16_t *)W + (size_t)r * D + c));
-            const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                w[2 * i] = __uint_as_float(uu[i] << 16);
-                w[2 * i + 1] = __uint_as_float(uu[i] & 0xFFFF0000u);
-            }
-        } else {
-            const float4 a = __ldg((const float4 *)((const float *)W + (size_t)r * D + c));
-            const float4 b = __ldg((const float4 *)((const float *)W + (size_t)r * D + c + 4));
-            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const float4 x0 = *(const float4 *)(sX + t * D + c), x1 = *(const float4 *)(sX + t * D + c + 4);
-            acc[t] = fmaf(w[0], x0.x, acc[t]);
-            acc[t] = fmaf(w[1], x0.y, acc[t]);
-            acc[t] = fmaf(w[2], x0.z, acc[t]);
-            acc[t] = fmaf(w[3], x0.w, acc[t]);
-            acc[t] = fmaf(w[4], x1.x, acc[t]);
-            acc[t] = fmaf(w[5], x1.y, acc[t]);
-            acc[t] = fmaf(w[6], x1.z, acc[t]);
-            acc[t] = fmaf(w[7], x1.w, acc[t]);
-        }
-    }
-}
-
 // sU[f][t0 + g] = w_(f0 + f) . x_g for 16 MT of a warp's features and 8 tokens (x: this lane's token row
 // g, NULL for none; g = lane / 4); returns |x_g|^2. As warp MMAs: bf16 products are exact, fp32 rows are
 // hi + lo in tf32 (three products, 2^-22). K runs in the order in which 16-byte loads hand it out, the
