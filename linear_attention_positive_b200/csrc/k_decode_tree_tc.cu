@@ -14,11 +14,12 @@
 // Precision: a, b and s S' enter the MMAs as hi + lo, two fp16 values (22 bits), products hi hi,
 // hi lo, lo hi; a and b are scaled by 2^15, so that a term 2^-18 below its maximum keeps all 22 bits
 // and fp16's smallest step is an error of at most 2^-40 of the maximum. s S' is scaled by its first
-// 64 features' largest magnitude to about 1. Weights of values are three bf16 parts against the bf16
-// values. The steps' error in a row's denominator is at most
-//   2^-40 sum_{j in J(i)} 2^G_j (sum_r a_jr + sum_r b_ir);
-// a row where that bound exceeds 2^-14 of the denominator (its own terms lie far below the scales of
-// other rows'), and every row of a head with a non-finite value or s S' beyond fp16's range, is
+// 64 features' largest magnitude to about 2^6 (1000 times that still fits). Weights of values are three
+// bf16 parts against the bf16 values. The steps' error in a row is at most
+//   2^-40 sum_{j in J(i)} 2^G_j (sum_r a_jr + sum_r b_ir) + 2^-31 sum_r b_ir
+// (the second part: s S', at most 2^-25 2^-6 of its largest magnitude); a row where that bound exceeds
+// 2^-14 of the denominator (its own terms lie far below the scales of other rows'), and every row of a
+// head with a non-finite value or s S' beyond fp16's range, is
 // computed by tree_row_exact. (A floor under the denominator instead of the bound sent one row in a
 // thousand there at d = 128 behind short contexts, and a row takes as long as a head.)
 //
@@ -43,6 +44,8 @@ namespace favor {
 constexpr int kTreeTcThreads = 512;
 // Keys at most this far (log2) above the state's features leave X_r as it is.
 constexpr float kTreeTcRaise = 10.f;
+// s S' is scaled so that its first 64 features' largest magnitude is about 2^this.
+constexpr float kTreeTcState = 6.f;
 
 template <int D_, bool STACK_>
 struct TreeTc {
@@ -175,7 +178,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
     const bool is_key = !STACK || (warp & 3) < 2, is_query = !STACK || (warp & 3) >= 2;
     const uint32_t tL = tmem + (((uint32_t)(warp & 3) * 32u) << 16);
     float eN = 0.f;     // -|k|^2/2 of this thread's key, log2 units
-    float shift = 0.f;  // s S' enters as 2^-shift of itself
+    float shift = 0.f;  // s S' enters as 2^(kTreeTcState - shift) of itself
     bool v_asked = false;
     auto load_values = [&]() {
         if (warp == 0 && elect_one()) {
@@ -258,7 +261,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
             float mx = sRed[0];
 #pragma unroll
             for (int w = 1; w < min(D / 8, kTreeTcThreads / 32); ++w) mx = fmaxf(mx, sRed[w]);
-            // its exponent (|shift| <= 110 keeps 2^-shift s_r a normal number)
+            // its exponent (within 110, so that the scale of s_r S' stays a normal number)
             shift = mx > 0.f ? (float)min(max((int)(__float_as_uint(mx) >> 23) - 127, -110), 110) : 0.f;
         }
 
@@ -346,7 +349,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
 
         float den_s[2] = {0.f, 0.f}, sum_a[2] = {0.f, 0.f}, sum_q[2] = {0.f, 0.f};  // 2^15 y_i, sum_r a_jr and b_ir, of this thread's features
         float(&sum_b)[2] = STACK ? sum_a : sum_q;  // (a thread of a stacked tile has a key or a query)
-        const float up = exp2f(-shift);
+        const float up = exp2f(kTreeTcState - shift);
         // 16 features from TMEM: 2^(15 + P + sgn X - max) as hi + lo
         auto split = [&](uint32_t col, int f, float sgn, float c, uint32_t(&hi)[8], uint32_t(&lo)[8], float(&sum)[2], bool state) {
             float v[16];
@@ -501,7 +504,8 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
         if (is_query) {
             constexpr int KT = MR / 4;  // keys a thread takes
             const float sb = (sSum[512 + row] + sSum[640 + row]) + (sSum[768 + row] + sSum[896 + row]);
-            float den = has_state ? (den_s[0] + den_s[1]) * 0x1p-15f : 0.f, err = 0.f;
+            float den = has_state ? (den_s[0] + den_s[1]) * 0x1p-15f : 0.f;
+            float err = has_state && cg == 0 ? sb * 0x1p-21f : 0.f;  // (S''s own: 2^-31 of sb, in err's units)
             const int j0 = KT * cg;
             const uint32_t seen = sAnc[row * (MR / 32) + (j0 >> 5)] >> (j0 & 31);
 #pragma unroll
@@ -570,7 +574,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
             // (measured against 64 bits at m = 32, 128, 256: 1.9e-7, 3.3e-7, 7.3e-7 low in all), while y_i is
             // summed with rounding; what is expected to be missing is added back.
             const float lost = 1.8e-8f * (float)(min(m, 64 * NSB) / 16 + 3 * max(m - 64 * NSB, 0) / 16);
-            const float fy = ex2_approx(shift - 15.f) * (1.f + lost);
+            const float fy = ex2_approx(shift - kTreeTcState - 15.f) * (1.f + lost);
             constexpr int CT = D / 4;  // columns a thread takes
 #pragma unroll
             for (int q = 0; q < CT; q += 16) {

@@ -183,6 +183,59 @@ def test_tree_unseen_nodes_with_far_larger_logits(cuda_device, dtype, scale, pri
     assert rel_max_err(got, ref) <= 8 * TOL
 
 
+def tree_from_state(x, state, parents, n_nodes, heads):
+    """Rows by the fp64 definition over the sums a device state holds, for some (b, h)."""
+    S, z = x.gpu_state(state)
+    return {(b, h): speculative.decode_tree(S[b, h], z[b, h], *(x.head(t, b, h)[: n_nodes[b]] for t in (x.q, x.k, x.v)),
+                                            x.W64, list(parents[b][: n_nodes[b]])) for b, h in heads}
+
+
+@pytest.mark.parametrize("T,d,m", [(64, 64, 256), (64, 128, 256), (100, 64, 256), (100, 128, 128), (17, 64, 96), (6, 64, 256)])
+def test_tree_of_a_full_batch(cuda_device, T, d, m):
+    """More heads than fit the device at once, sequences cut differently (some heads checked)."""
+    B, H = 25, 16
+    x = Problem(B, H, T, d, m, "bf16", cuda_device, prior=0, seed=T + d)
+    state = api.decode_extend(x.tokens(70, d ** -0.25), x.tokens(70, 1.0), x.W, x.state)
+    parents = random_parents(B, T, seed=T)
+    counts = np.random.default_rng(T).integers(0, T + 1, B)
+    counts[:4] = T, 0, 1, T - 1
+    out = torch.full((B, H, T, d), 7.0, device=cuda_device)
+    api.decode_tree(x.q, x.k, x.v, x.W, state, i32(parents, cuda_device), n_nodes=i32(counts, cuda_device), out=out)
+    status_ok()
+    got = out.double().cpu().numpy()
+    heads = [(0, 0), (0, 15), (2, 5), (3, 1), (9, 9), (17, 3), (24, 15)]
+    for (b, h), ref in tree_from_state(x, state, parents, counts, heads).items():
+        assert rel_max_err(got[b, h, : counts[b]], ref) <= TOL if counts[b] else True
+    for b in range(B):
+        assert (got[b, :, counts[b]:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("prior", [1, 3, 12])
+@pytest.mark.parametrize("T,d", [(64, 64), (64, 128), (120, 64), (3, 64)])
+def test_tree_behind_a_short_context(cuda_device, dtype, prior, T, d):
+    """The tree's keys lie far above what a few tokens left in the state."""
+    x = Problem(2, 3, T, d, 256, dtype, cuda_device, prior=prior, seed=prior + T)
+    parents = random_parents(2, T, seed=T)
+    out = api.decode_tree(x.q, x.k, x.v, x.W, x.state, i32(parents, cuda_device))
+    status_ok()
+    assert rel_max_err(out.double().cpu().numpy(), x.oracle_tree(parents)) <= TOL
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("factor", [2.0**40, 2.0**-40, 0.0])
+def test_tree_over_features_of_very_different_sums(cuda_device, dtype, factor):
+    """S' of the features from 64 on scaled away from the others' (also beyond what fp16 spans)."""
+    x = Problem(1, 2, 40, 64, 192, dtype, cuda_device, seed=50)
+    state = x.state.clone()
+    state.view(2, 66, 192)[:, :64, 64:] *= factor
+    parents = random_parents(1, 40, seed=50)
+    out = api.decode_tree(x.q, x.k, x.v, x.W, state, i32(parents, cuda_device)).double().cpu().numpy()
+    status_ok()
+    for (b, h), ref in tree_from_state(x, state, parents, [40], [(0, 0), (0, 1)]).items():
+        assert rel_max_err(out[b, h], ref) <= TOL
+
+
 def test_tree_bad_parents_and_counts_are_recorded(cuda_device):
     T = 20
     x = Problem(2, 2, T, 64, 128, "bf16", cuda_device, seed=8)
@@ -250,6 +303,32 @@ def test_extend_runs_of_many_tiles(cuda_device, L, d, m):
     for b, h in [(0, 0), (0, 15), (1, 7), (2, 3), (3, 1), (11, 9), (19, 15)]:
         n = int(counts[b])
         Sr, zr = speculative.decode_extend(np.zeros((m, d)), np.zeros(m), x.head(x.k, b, h)[:n], x.head(x.v, b, h)[:n], x.W64)
+        assert np.abs(S[b, h] - Sr).max() <= TOL * np.abs(Sr).max()
+        assert np.abs(z[b, h] - zr).max() <= TOL * np.abs(zr).max()
+
+
+@pytest.mark.parametrize("dtype,indexed", [("f32", False), ("f32", True), ("bf16", True)])
+@pytest.mark.parametrize("L,d,m", [(100, 64, 256), (100, 128, 96), (33, 128, 256), (17, 64, 32)])
+def test_extend_rows_of_a_full_batch(cuda_device, dtype, indexed, L, d, m):
+    """More heads than fit the device at once, counts cut differently, fp32 or by index (some heads checked)."""
+    B, H = 25, 16
+    x = Problem(B, H, L, d, m, dtype, cuda_device, prior=0, seed=L + d)
+    g = np.random.default_rng(L)
+    counts = g.integers(0, L + 1, B)
+    counts[:3] = L, 0, 1
+    index = np.stack([g.permutation(L) for _ in range(B)])
+    state = x.state
+    for _ in range(2):  # into the empty state, then onto itself
+        state = api.decode_extend(x.k, x.v, x.W, state, index=i32(index, cuda_device) if indexed else None,
+                                  counts=i32(counts, cuda_device))
+    status_ok()
+    S, z = x.gpu_state(state)
+    for b, h in [(0, 0), (0, 15), (1, 7), (2, 3), (8, 1), (16, 9), (24, 15)]:
+        n = int(counts[b])
+        at = index[b, :n] if indexed else np.arange(n)
+        Sr, zr = np.zeros((m, d)), np.zeros(m)
+        for _ in range(2):
+            Sr, zr = speculative.decode_extend(Sr, zr, x.head(x.k, b, h)[at], x.head(x.v, b, h)[at], x.W64)
         assert np.abs(S[b, h] - Sr).max() <= TOL * np.abs(Sr).max()
         assert np.abs(z[b, h] - zr).max() <= TOL * np.abs(zr).max()
 
