@@ -41,7 +41,6 @@
 
 namespace favor {
 
-constexpr int kTreeTcThreads = 512;
 // Keys at most this far (log2) above the state's features leave X_r as it is.
 constexpr float kTreeTcRaise = 10.f;
 // s S' is scaled so that its first 64 features' largest magnitude is about 2^this.
@@ -50,6 +49,9 @@ constexpr float kTreeTcState = 6.f;
 template <int D_, bool STACK_>
 struct TreeTc {
     static constexpr int D = D_, NB = D / 64;
+    // Column groups of a TMEM lane, a warpgroup each. Two CTAs an SM leave 64 registers to 512 threads, and
+    // their spills go to L2 (shared memory takes all of L1): 96 us for 1024 heads, 77 with 256 threads.
+    static constexpr int NCG = (STACK_ && D == 64) ? 2 : 4, THREADS = 128 * NCG;
     static constexpr int MR = STACK_ ? 64 : 128;             // key rows
     static constexpr uint32_t BLK = 128 * 128;               // 64 columns of a 128-row tile
     static constexpr uint32_t KQ = (STACK_ ? 1 : 2) * NB * BLK;
@@ -75,20 +77,20 @@ __device__ __forceinline__ int order_bits(float x) {
 __device__ __forceinline__ float from_order_bits(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
 template <int D, bool STACK>
-__global__ void __launch_bounds__(kTreeTcThreads, (STACK && D == 64) ? 2 : 1)
+__global__ void __launch_bounds__(TreeTc<D, STACK>::THREADS, (STACK && D == 64) ? 2 : 1)
 k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                  const __grid_constant__ CUtensorMap mapV, const __grid_constant__ CUtensorMap mapW,
                  const __grid_constant__ CUtensorMap mapS, TreeParams p) {
     using C = TreeTc<D, STACK>;
-    constexpr int NB = C::NB, MR = C::MR, NSB = C::NSB;
+    constexpr int NB = C::NB, MR = C::MR, NSB = C::NSB, NCG = C::NCG;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sKQ = smem, *sW = smem + C::OFF_W, *sXH = smem + C::OFF_XH, *sXL = smem + C::OFF_XL;
     uint8_t *sXL1 = C::OVER ? sW : sXL + C::XB;
     uint8_t *sV = sKQ;                                    // the values take the keys' place
     float *sX = (float *)(smem + C::OFF_F), *sZ = sX + 256, *sFac = sZ + 256;  // X_r, s_r z'_r, s_r
-    float *sMx = sFac + 256;                              // [keys, queries][4 column groups][128] maxima
-    float *sDen = sMx, *sErr = sMx + 4 * 128;             // then [4][128] parts of denominators and their errors
+    float *sMx = sFac + 256;                              // [keys, queries][column group][128] maxima
+    float *sDen = sMx, *sErr = sMx + 4 * 128;             // then [column group][128] parts of denominators and their errors
     float *sSum = sMx + 8 * 128;                          // [keys, queries][4][128] sums of a and b
     float *sGe = sSum + 8 * 128;                          // 2^(G_j - 30)
     float *sRed = sGe + 128;                              // [16] warp maxima
@@ -146,7 +148,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
         Dr = zp[m + tid];
     }
     int ptr = -1;
-    const int node = tid - 256;  // the threads that form J's rows
+    const int node = tid - C::THREADS / 2;  // the threads that form J's rows
     if (node >= 0 && node < n) ptr = tree_parent(p.parents + (size_t)b * T, node);
 
     tc_fence_before();
@@ -154,7 +156,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    // (descriptors are formed where they are used: 64 registers a thread leave no room to keep them)
+    // (descriptors are formed where they are used, by one warp)
     auto logits = [&](int h, uint32_t col) {  // warp 0
         constexpr uint32_t idesc_p = make_idesc(128, 128, kFmtBF16, 0, 0);
         const uint64_t dKQ = make_sdesc(smem_u32(sKQ), 16, 1024), dW = make_sdesc(smem_u32(sW), 16, 1024);
@@ -234,7 +236,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
         if (!wait(&s_full[0], 0)) break;
         {
             float mx = 0.f;
-            for (int rg = warp; rg < D / 8; rg += kTreeTcThreads / 32) {
+            for (int rg = warp; rg < D / 8; rg += C::THREADS / 32) {
                 const int q = lane >> 3;
                 const uint8_t *src = (q < 2 ? sXH : sXL) + MR * 128 + rg * 1024;
 #pragma unroll
@@ -260,7 +262,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
         {
             float mx = sRed[0];
 #pragma unroll
-            for (int w = 1; w < min(D / 8, kTreeTcThreads / 32); ++w) mx = fmaxf(mx, sRed[w]);
+            for (int w = 1; w < min(D / 8, C::THREADS / 32); ++w) mx = fmaxf(mx, sRed[w]);
             // its exponent (within 110, so that the scale of s_r S' stays a normal number)
             shift = mx > 0.f ? (float)min(max((int)(__float_as_uint(mx) >> 23) - 127, -110), 110) : 0.f;
         }
@@ -268,12 +270,12 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
         // row maxima of P + sgn X over this thread's columns of a half
         auto row_max = [&](uint32_t col, int h, float sgn) {
             float mx = -INFINITY;
-            const int f0 = 128 * h + 32 * cg;
-            if (f0 >= m) return mx;
+            const int f0 = 128 * h + 128 / NCG * cg;
 #pragma unroll 1
-            for (int q = 0; q < 32; q += 16) {
+            for (int q = 0; q < 128 / NCG; q += 16) {
+                if (f0 + q >= m) break;
                 float v[16];
-                tmem_ld16(tL + col + 32 * cg + q, v);
+                tmem_ld16(tL + col + 128 / NCG * cg + q, v);
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
                     const float4 x = *(const float4 *)(sX + f0 + q + e);
@@ -296,11 +298,17 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
             if (is_query) {
                 float x = row_max(C::T_Q, 0, 1.f);
                 if (nh == 2) x = fmaxf(x, row_max(C::T_H + C::T_Q, 1, 1.f));
-                sMx[(4 + cg) * 128 + row] = x;
+                sMx[(NCG + cg) * 128 + row] = x;
             }
             __syncthreads();
-            if (is_key) g2 = ceilf(fmaxf(fmaxf(sMx[row], sMx[128 + row]), fmaxf(sMx[256 + row], sMx[384 + row])));
-            if (is_query) f2 = ceilf(fmaxf(fmaxf(sMx[512 + row], sMx[640 + row]), fmaxf(sMx[768 + row], sMx[896 + row])));
+            auto over_groups = [&](const float *at) {
+                float x = at[row];
+#pragma unroll
+                for (int i = 1; i < NCG; ++i) x = fmaxf(x, at[i * 128 + row]);
+                return ceilf(x);
+            };
+            if (is_key) g2 = over_groups(sMx);
+            if (is_query) f2 = over_groups(sMx + NCG * 128);
         };
         bool raise = any_empty;
         if (!raise) {
@@ -312,12 +320,12 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
             float *sE = (float *)sXH;  // [4][256], the lane quarters' maxima
             if (is_key) {
                 for (int h = 0; h < nh; ++h) {
-                    const int f0 = 128 * h + 32 * cg;
-                    if (f0 >= m) break;
+                    const int f0 = 128 * h + 128 / NCG * cg;
 #pragma unroll 1
-                    for (int q = 0; q < 32; q += 16) {
+                    for (int q = 0; q < 128 / NCG; q += 16) {
+                        if (f0 + q >= m) break;
                         float v[16], mine = -INFINITY;
-                        tmem_ld16(tL + h * C::T_H + C::T_K + 32 * cg + q, v);
+                        tmem_ld16(tL + h * C::T_H + C::T_K + 128 / NCG * cg + q, v);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float u = fmaf(v[e], kLog2e, eN);
@@ -382,8 +390,8 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
             const int c1 = min(nch, c0 + NSB), h = c0 >> 1;
             // exponentials: a to shared memory, b in place of its logits
 #pragma unroll 1
-            for (int u = 0; u < NSB; ++u) {
-                const int col = NSB == 2 ? 32 * cg + 16 * u : 64 * (c0 & 1) + 16 * cg;  // in this half
+            for (int u = 0; u < 4 * NSB / NCG; ++u) {
+                const int col = (NSB == 2 ? 0 : 64 * (c0 & 1)) + 64 * NSB / NCG * cg + 16 * u;  // in this half
                 const int f = 128 * h + col, blk = NSB == 2 ? col >> 6 : 0;
                 if (f >= m) break;
                 uint32_t hi[8], lo[8];
@@ -410,7 +418,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
                 if (!wait(&s_full[c % NSB], (c / NSB) & 1)) break;
             if (!ok) break;
             bool bad = false;
-            for (int t = warp; t < (c1 - c0) * (D / 8); t += kTreeTcThreads / 32) {
+            for (int t = warp; t < (c1 - c0) * (D / 8); t += C::THREADS / 32) {
                 const int c = c0 + t / (D / 8), rg = t % (D / 8), s = c % NSB, q = lane >> 3, r = 64 * c + 16 * q;
                 uint8_t *xh = sXH + s * C::XB + MR * 128 + rg * 1024, *xl = (s == 0 ? sXL : sXL1) + MR * 128 + rg * 1024;
                 uint32_t hi[8], lo[8];
@@ -481,13 +489,13 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
         }
         if (!ok) break;
         if (is_key) sSum[cg * 128 + row] = sum_a[0] + sum_a[1];
-        if (is_query) sSum[(4 + cg) * 128 + row] = sum_b[0] + sum_b[1];
+        if (is_query) sSum[(NCG + cg) * 128 + row] = sum_b[0] + sum_b[1];
 
         // values: rows past the tree are not the tree's; non-finite ones must not meet a zero weight
         if (!wait(v_full, 0)) break;
         {
             bool bad = false;
-            for (int i = tid; i < NB * MR * 8; i += kTreeTcThreads) {
+            for (int i = tid; i < NB * MR * 8; i += C::THREADS) {
                 uint4 *at = (uint4 *)(sV + (size_t)i * 16);
                 if (((i >> 3) & (MR - 1)) >= n) {
                     *at = make_uint4(0u, 0u, 0u, 0u);
@@ -502,8 +510,15 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
         }
         // weights of the visible nodes
         if (is_query) {
-            constexpr int KT = MR / 4;  // keys a thread takes
-            const float sb = (sSum[512 + row] + sSum[640 + row]) + (sSum[768 + row] + sSum[896 + row]);
+            constexpr int KT = MR / NCG;  // keys a thread takes
+            static_assert(KT <= 32, "one word of J");
+            auto over_groups = [&](const float *at, int i) {
+                float x = at[i];
+#pragma unroll
+                for (int k = 1; k < NCG; ++k) x += at[k * 128 + i];
+                return x;
+            };
+            const float sb = over_groups(sSum + NCG * 128, row);
             float den = has_state ? (den_s[0] + den_s[1]) * 0x1p-15f : 0.f;
             float err = has_state && cg == 0 ? sb * 0x1p-21f : 0.f;  // (S''s own: 2^-31 of sb, in err's units)
             const int j0 = KT * cg;
@@ -522,7 +537,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
                         float w = 0.f;
                         if ((seen >> (q + e + k)) & 1u) {
                             w = v[e + k] * sGe[j];
-                            err = fmaf(sGe[j], sb + (sSum[j] + sSum[128 + j]) + (sSum[256 + j] + sSum[384 + j]), err);
+                            err = fmaf(sGe[j], sb + over_groups(sSum, j), err);
                         }
                         den += w;
                         // w in three bf16 parts of 8 bits, by truncation
@@ -559,8 +574,12 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
         bool good = false;
         float inv = 0.f;
         if (is_query) {
-            const float den = (sDen[row] + sDen[128 + row]) + (sDen[256 + row] + sDen[384 + row]);
-            const float err = (sErr[row] + sErr[128 + row]) + (sErr[256 + row] + sErr[384 + row]);
+            float den = sDen[row], err = sErr[row];
+#pragma unroll
+            for (int k = 1; k < NCG; ++k) {
+                den += sDen[k * 128 + row];
+                err += sErr[k * 128 + row];
+            }
             good = den >= 1e-30f && den < INFINITY && den >= err * 0x1p-11f;
             inv = 1.f / den;
         }
@@ -575,7 +594,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
             // summed with rounding; what is expected to be missing is added back.
             const float lost = 1.8e-8f * (float)(min(m, 64 * NSB) / 16 + 3 * max(m - 64 * NSB, 0) / 16);
             const float fy = ex2_approx(shift - kTreeTcState - 15.f) * (1.f + lost);
-            constexpr int CT = D / 4;  // columns a thread takes
+            constexpr int CT = D / NCG;  // columns a thread takes
 #pragma unroll
             for (int q = 0; q < CT; q += 16) {
                 const int c0 = cg * CT + q;
@@ -595,11 +614,11 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
         }
         __syncthreads();
         float *out = p.out + (size_t)bh * T * D;
-        for (int i = tid; i < n * (D / 4); i += kTreeTcThreads) {
+        for (int i = tid; i < n * (D / 4); i += C::THREADS) {
             const int r = i / (D / 4), c = i % (D / 4);
             if (sPtr[r]) *(float4 *)(out + (size_t)i * 4) = *(const float4 *)(sOut + r * D + ((c ^ (r & 7)) << 2));
         }
-        for (int r = warp; r < n; r += kTreeTcThreads / 32)
+        for (int r = warp; r < n; r += C::THREADS / 32)
             if (!sPtr[r]) tree_row_exact<D>(p, bh, r, sPar);
     } while (false);
 
@@ -628,7 +647,7 @@ static cudaError_t launch_tree_tc_t(const CUtensorMap &mQ, const CUtensorMap &mK
     const cudaError_t e =
         cudaFuncSetAttribute(k_decode_tree_tc<D, STACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::BYTES);
     if (e != cudaSuccess) return e;
-    k_decode_tree_tc<D, STACK><<<p.B * p.H, kTreeTcThreads, C::BYTES, st>>>(mQ, mK, mV, mW, mS, p);
+    k_decode_tree_tc<D, STACK><<<p.B * p.H, C::THREADS, C::BYTES, st>>>(mQ, mK, mV, mW, mS, p);
     return cudaGetLastError();
 }
 
