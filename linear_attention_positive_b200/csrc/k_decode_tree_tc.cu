@@ -389,7 +389,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
         for (int c0 = 0; c0 < nch; c0 += NSB) {  // steps of 64 NSB features
             const int c1 = min(nch, c0 + NSB), h = c0 >> 1;
             // exponentials: a to shared memory, b in place of its logits
-#pragma unroll 1
+#pragma unroll 2
             for (int u = 0; u < 4 * NSB / NCG; ++u) {
                 const int col = (NSB == 2 ? 0 : 64 * (c0 & 1)) + 64 * NSB / NCG * cg + 16 * u;  // in this half
                 const int f = 128 * h + col, blk = NSB == 2 ? col >> 6 : 0;
