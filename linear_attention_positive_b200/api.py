@@ -392,11 +392,16 @@ def _tokens(first, rest, W, state):
     return (B, H, L, d, m, _dtype_code(first)), device
 
 
-def _launch(what, f, device, stream, *args):
+def _launch(what, f, device, stream, own, *args):
     """Calls an entry point whose last argument is the stream (default: the current one of the tensors'
-    device) with that device current."""
+    device) with that device current. ``own``: tensors allocated for the call on the current stream; one
+    that another stream uses must not be handed out again before that stream is done with it."""
     torch = _torch()
-    raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+    current = torch._C._cuda_getCurrentRawStream(device.index)
+    raw = current if stream is None else stream.cuda_stream
+    if raw != current:
+        for t in own:
+            t.record_stream(stream)
     if torch._C._cuda_getDevice() == device.index:
         st = f(*args, raw)
     else:
@@ -417,11 +422,13 @@ def decode_tree(q, k, v, W, state, parents, n_nodes=None, out=None, stream=None)
     i32 = torch.int32
     _fits("parents", parents, (dims[0], dims[2]), i32, device)
     nodes = _opt_ptr("n_nodes", n_nodes, (dims[0],), i32, device)
+    own = ()
     if out is None:
         out = torch.empty(q.shape, dtype=torch.float32, device=device)
+        own = (out,)
     else:
         _fits("out", out, q.shape, torch.float32, device)
-    _launch("favor_decode_tree", library().favor_decode_tree, device, stream, _shape_ref(Shape, *dims), q.data_ptr(),
+    _launch("favor_decode_tree", library().favor_decode_tree, device, stream, own, _shape_ref(Shape, *dims), q.data_ptr(),
             k.data_ptr(), v.data_ptr(), W.data_ptr(), state.data_ptr(), parents.data_ptr(), nodes, out.data_ptr())
     return out
 
@@ -446,13 +453,14 @@ def decode_extend(k, v, W, state, index=None, counts=None, workspace=None, strea
         n_index = index.shape[1]
         _fits("index", index, (dims[0], n_index), i32, device)
         index_ptr = index.data_ptr()
-    n_tok = _opt_ptr("counts", counts, (dims[0],), i32, device)
+    n_tok, own = _opt_ptr("counts", counts, (dims[0],), i32, device), ()
     if workspace is None:
         ws_n = _extend_workspace(device.index, n_index, *dims)
         if ws_n == 0:
             raise FavorError(FAVOR_ERR_UNSUPPORTED, "favor_decode_extend_workspace_size")
         workspace = torch.empty(ws_n, dtype=torch.uint8, device=device)
-    _launch("favor_decode_extend", library().favor_decode_extend, device, stream, _shape_ref(Shape, *dims),
+        own = (workspace,)
+    _launch("favor_decode_extend", library().favor_decode_extend, device, stream, own, _shape_ref(Shape, *dims),
             k.data_ptr(), v.data_ptr(), W.data_ptr(), index_ptr, n_index, n_tok, state.data_ptr(),
             workspace.data_ptr(), workspace.numel())
     return state
@@ -477,7 +485,7 @@ def decode_verify(parents, tokens, p, u, r, q=None, n_nodes=None, stream=None):
     _fits("u", u, nodes, f32, device)
     _fits("r", r, row, f32, device)
     path, n_path, token = parents.new_empty(nodes), parents.new_empty(row), parents.new_empty(row)
-    _launch("favor_decode_verify", library().favor_decode_verify, device, stream,
+    _launch("favor_decode_verify", library().favor_decode_verify, device, stream, (path, n_path, token),
             _shape_ref(VerifyShape, B, T, V, _dtype_code(p)), parents.data_ptr(), tokens.data_ptr(), used, p.data_ptr(),
             draft, u.data_ptr(), r.data_ptr(), path.data_ptr(), n_path.data_ptr(), token.data_ptr())
     return path, n_path, token

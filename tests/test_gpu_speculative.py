@@ -642,6 +642,38 @@ def test_another_stream_and_captured_graphs(cuda_device):
     status_ok()
 
 
+def test_calls_given_a_stream(cuda_device):
+    """stream=: the same bits as on the current stream, though the current one keeps allocating and writing
+    (what the call allocated for itself is not handed out while the other stream uses it)."""
+    x = Problem(1, 4, 4000, 64, 256, "bf16", cuda_device, prior=0, seed=60)
+    y = draft(4, 20, 20000, "f32", cuda_device, seed=61)
+    parents, tokens = i32(y["parents"], cuda_device), i32(y["tokens"], cuda_device)
+    u, r = (torch.tensor(y[k], device=cuda_device) for k in "ur")
+    want_state = api.decode_extend(x.k, x.v, x.W, x.state.clone())
+    want = api.decode_verify(parents, tokens, y["p"], u, r, q=y["q"])
+    t = [z[:, :, :40].contiguous() for z in (x.q, x.k, x.v)]
+    tree = i32(random_parents(1, 40), cuda_device)
+    want_out = api.decode_tree(*t, x.W, want_state, tree)
+    side = torch.cuda.Stream()
+    n = api.library().favor_decode_extend_workspace_size(api.ctypes.byref(api.make_shape(1, 4, 4000, 64, 256, api.FAVOR_BF16)), 0)
+    for _ in range(3):
+        state = x.state.clone()
+        side.wait_stream(torch.cuda.current_stream())
+        for _ in range(4):  # the side stream is busy when the calls are made
+            torch.cuda._sleep(200000)
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(200000)
+        api.decode_extend(x.k, x.v, x.W, state, stream=side)
+        junk = [torch.full((n,), 255, dtype=torch.uint8, device=cuda_device) for _ in range(3)]
+        got = api.decode_verify(parents, tokens, y["p"], u, r, q=y["q"], stream=side)
+        out = api.decode_tree(*t, x.W, state, tree, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(state, want_state) and torch.equal(out, want_out)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        del junk
+    status_ok()
+
+
 def test_binding_refuses_what_does_not_fit(cuda_device):
     x = Problem(2, 2, 6, 64, 128, "bf16", cuda_device, prior=0)
     parents = i32(random_parents(2, 6), cuda_device)
