@@ -1122,8 +1122,9 @@ bool decode_supported(const favor_shape *s) {
 }
 
 // Whether a tree goes to the tensor cores' tiles (bf16). Up to 4 nodes the few-node kernel is faster at
-// any batch (1024 heads, d = 64, m = 256: 42 us against 87), up to 16 the row kernel while its CTAs fit
-// the SMs once (8 heads: 13 us against 18 at 8 nodes, 16 against 18 at 16; 1024 heads: 90 against 87).
+// any batch (d = 64, m = 256: 54 us for 1024 heads of 4 nodes, 8 for 8 heads; the tiles about 70 and 17
+// at any size up to 20 nodes), up to 16 the row kernel while its CTAs fit the SMs once (8 heads: 13 us at
+// 8 nodes, 16 at 16; but 90 and 108 for 1024 heads).
 bool tree_on_tiles(const favor_shape *s) {
     if (s->dtype != FAVOR_BF16 || s->L <= 4) return false;
     return s->L > kRowsTile || (long long)s->B * s->H * (s->d / kRowsCols) > num_sms();

@@ -282,7 +282,8 @@ __device__ __forceinline__ void halving_sum(float (&v)[TQ], int lane) {
 // One CTA per (head, 64 value columns), one thread per feature, all nodes at once, fp32 throughout. The
 // thread's 64 entries of S' are asked for before anything else and arrive under the projections; sums
 // over features are halving exchanges inside each warp, then across warps through shared memory. Small
-// trees are bound by the latency of that one chain: about 1 us for the loads and as much for the rest.
+// trees are bound by the latency of that one chain: 5.5 us for one node in 8 heads at d = 64, m = 256 (22 with
+// the state's columns loaded where they are used).
 
 constexpr int kFewCols = 64;
 
@@ -453,7 +454,8 @@ static cudaError_t launch_tree_few(const TreeParams &p, cudaStream_t st) {
 // fragments in registers; the products over the features, [16 rows x m] [m x (64 state columns + keys)],
 // as tf32 warp MMAs with both sides hi + lo (three products, 2^-22: fp32's precision), a group of 8
 // columns a warp. A warp's state columns are asked for before anything else. fp32 trees of any size,
-// and bf16 ones too small for whole tiles, where the latency of this chain (five barriers) is the bound.
+// and bf16 ones too small for whole tiles, where the latency of this chain (five barriers) is the bound: 17 us
+// for fp32 trees of up to 33 nodes in 64 heads (34 as sums on CUDA cores).
 
 constexpr int kRowsThreads = 256;
 constexpr int kRowsTile = 16;
