@@ -23,8 +23,11 @@
 //
 // Warps 0-3: exponentials and z_r. Warps 4, 5: |k|^2 and the norms' extension; 6, 7: V -> fp16 (one after
 // the other in all four they held up the exponents: 4200 cycles a tile against 1550); 4-7: S. Warp 8: K
-// and W copies, P; warp 9: V copies, the accumulator. Every barrier that a group waits on is at most one phase ahead of it, but d_full, which
-// has four slots: the exponent warps may be two tiles ahead of warps 4-7 there, warps 6, 7 four of 4, 5.
+// and W copies, P; warp 9: V copies, the accumulator. Every barrier that a group waits on is at most one
+// phase ahead of it, but d_full, which has four slots. What the tiles tell each other through shared memory
+// (D_r, whether it changed, b) lies in rings of kExtRing tiles: the exponent warps may be five tiles ahead of
+// warps 6, 7, each of which reads a tile's entries only after converting a later tile, and so may the
+// other warp of the two (tests/test_extend_tile_protocol.py walks all these orderings).
 
 #include "common.cuh"
 
@@ -32,6 +35,7 @@ namespace favor {
 
 constexpr int kExtTile = 64;
 constexpr int kExtFlush = 16;
+constexpr int kExtRing = 8;
 
 template <int D_>
 struct ExtTc {
@@ -41,8 +45,8 @@ struct ExtTc {
     static constexpr int THREADS = 320;
     static constexpr uint32_t T_P = 0, T_ACC = 128;  // TMEM columns: two tiles of P, the accumulator
     static constexpr size_t OFF_K = WT, OFF_V = OFF_K + NS * KT, OFF_KX = OFF_V + NS * KT, OFF_WX = OFF_KX + NS * KX,
-                            OFF_D = OFF_WX + 4096, OFF_F = OFF_D + 4 * 128 * 4, OFF_MISC = OFF_F + 128 * 8,
-                            OFF_BAR = OFF_MISC + 4 * (16 + 8 + 8), BYTES = OFF_BAR + 8 * (4 * NS + 2 + 2 + 2 + 4 + 5 + 4) + 8 + 1024;
+                            OFF_D = OFF_WX + 4096, OFF_F = OFF_D + kExtRing * 128 * 4, OFF_MISC = OFF_F + 128 * 8,
+                            OFF_BAR = OFF_MISC + 4 * 6 * kExtRing, BYTES = OFF_BAR + 8 * (4 * NS + 2 + 2 + 2 + 4 + 5 + 4) + 8 + 1024;
 };
 
 template <int D>
@@ -54,10 +58,10 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sW = smem, *sK = smem + C::OFF_K, *sV = smem + C::OFF_V, *sKx = smem + C::OFF_KX, *sWx = smem + C::OFF_WX;
-    float *sD = (float *)(smem + C::OFF_D);       // [tile % 4][128]: D_r
+    float *sD = (float *)(smem + C::OFF_D);       // [tile % kExtRing][128]: D_r
     float2 *sF = (float2 *)(smem + C::OFF_F);     // [128]: final factors of the run's and the old S'
-    int *sRaise = (int *)(smem + C::OFF_MISC);    // [tile % 4][warp]: some D_r of this warp's changes here
-    int *sScale = sRaise + 16, *sB = sScale + 8;  // [tile % 8]: b changes here; b
+    int *sRaise = (int *)(smem + C::OFF_MISC);    // [tile % kExtRing][warp]: some D_r of this warp's changes here
+    int *sScale = sRaise + 4 * kExtRing, *sB = sScale + kExtRing;  // [tile % kExtRing]: b changes here; b
     uint64_t *bars = (uint64_t *)(smem + C::OFF_BAR);
     uint64_t *k_full = bars, *v_full = k_full + NS, *k_conv = v_full + NS, *v_conv = k_conv + NS;
     uint64_t *p_full = v_conv + NS, *phi_full = p_full + 2, *s_done = phi_full + 2, *d_full = s_done + 2;
@@ -121,8 +125,8 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
     // whether S takes the accumulator before tile g adds to it (read after tile g's d_full, or its phi_full
     // and v_conv)
     auto flush_before = [&](int g) {
-        const int *r = sRaise + 4 * (g & 3);
-        return g > 0 && ((g % kExtFlush) == 0 || sScale[g & 7] != 0 || (r[0] | r[1] | r[2] | r[3]) != 0);
+        const int *r = sRaise + 4 * (g % kExtRing);
+        return g > 0 && ((g % kExtFlush) == 0 || sScale[g % kExtRing] != 0 || (r[0] | r[1] | r[2] | r[3]) != 0);
     };
 
     auto load = [&](const CUtensorMap *map, uint8_t *buf, uint64_t *bar, int g) {
@@ -230,9 +234,9 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                     raise = true;
                 }
                 umax = fmaxf(umax, um);
-                sD[(g & 3) * 128 + row] = Dr;
+                sD[(g % kExtRing) * 128 + row] = Dr;
                 raise = __any_sync(0xffffffffu, raise);
-                if (lane == 0) sRaise[4 * (g & 3) + warp] = raise;
+                if (lane == 0) sRaise[4 * (g % kExtRing) + warp] = raise;
                 __syncwarp();
                 mbar_arrive(&d_full[g & 3]);
                 float s0 = 0.f, s1 = 0.f;
@@ -340,15 +344,15 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 int bnext = 0;  // b of the tile before, then of this one
                 if (g > 0) {
                     if (!mbar_wait_all(&b_set[(g - 1) & 3], ((g - 1) >> 2) & 1, abort_flag)) return false;
-                    bnext = sB[(g - 1) & 7];
+                    bnext = sB[(g - 1) % kExtRing];
                 }
                 const bool finite = mx < 0x7F80u;
                 const int b = (int)(mx >> 7) - 127 - 12;
                 const bool changed = g == 0 || !finite || (mx != 0 && (b > bnext + 2 || b < bnext - 6));
                 if (changed) bnext = finite ? min(max(b, -100), 114) : 114;  // (not finite: S is not, either)
                 if (lane == 0) {
-                    sScale[g & 7] = changed;
-                    sB[g & 7] = bnext;
+                    sScale[g % kExtRing] = changed;
+                    sB[g % kExtRing] = bnext;
                 }
                 __syncwarp();
                 mbar_arrive(&b_set[g & 3]);
@@ -438,14 +442,16 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                     ok = g + lead >= n || ((g + lead) & 1) != (warp & 1) || conv_v(g + lead);
                 if (!ok || !(ok = mbar_wait_all(&d_full[g & 3], (g >> 2) & 1, abort_flag))) break;
                 const bool take = flush_before(g);
+                const float Dg = sD[(g % kExtRing) * 128 + row];  // (before the accumulator is given back)
+                const int bg = sB[g % kExtRing];
                 if (take) {
                     if (!(ok = mbar_wait_all(acc_full, flushes++ & 1, abort_flag))) break;
                     tc_fence_after();
                     flush();
                 }
                 if (take || g == 0) {
-                    Dacc = sD[(g & 3) * 128 + row];
-                    bcur = sB[g & 7];
+                    Dacc = Dg;
+                    bcur = bg;
                 }
             }
             if (ok && (ok = mbar_wait_all(acc_full, flushes & 1, abort_flag))) {
