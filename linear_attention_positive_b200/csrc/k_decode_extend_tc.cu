@@ -341,15 +341,24 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                     }
                 }
                 mx = __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
+                const bool finite = mx < 0x7F80u;
+                if (!finite) {  // the other entries' largest: infinities and NaN concern their own columns only
+                    mx = 0;
+#pragma unroll 1
+                    for (int i = 0; i < 64 * NB; ++i) {
+                        const uint32_t a = ((const uint32_t *)vt)[lane + 32 * i] & 0x7FFF7FFFu;
+                        mx = __vmaxu2(mx, a & ~__vcmpgeu2(a, 0x7F807F80u));
+                    }
+                    mx = __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
+                }
                 int bnext = 0;  // b of the tile before, then of this one
                 if (g > 0) {
                     if (!mbar_wait_all(&b_set[(g - 1) & 3], ((g - 1) >> 2) & 1, abort_flag)) return false;
                     bnext = sB[(g - 1) % kExtRing];
                 }
-                const bool finite = mx < 0x7F80u;
-                const int b = (int)(mx >> 7) - 127 - 12;
-                const bool changed = g == 0 || !finite || (mx != 0 && (b > bnext + 2 || b < bnext - 6));
-                if (changed) bnext = finite ? min(max(b, -100), 114) : 114;  // (not finite: S is not, either)
+                const int b = min(max((int)(mx >> 7) - 127 - 12, -100), 114);
+                const bool changed = g == 0 || (mx != 0 && (b > bnext + 2 || b < bnext - 6));
+                if (changed) bnext = b;
                 if (lane == 0) {
                     sScale[g % kExtRing] = changed;
                     sB[g % kExtRing] = bnext;
@@ -357,8 +366,8 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 __syncwarp();
                 mbar_arrive(&b_set[g & 3]);
                 mbar_arrive(&d_full[g & 3]);
+                const uint32_t low = (uint32_t)(112 + bnext) << 7, low2 = low | (low << 16);
                 if (finite) {
-                    const uint32_t low = (uint32_t)(112 + bnext) << 7, low2 = low | (low << 16);
 #pragma unroll 1
                     for (int q = 0; q < 4 * NB; ++q) {
                         uint4 x[4];
@@ -373,14 +382,13 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                             *(uint4 *)(vt + (size_t)(lane + 32 * (4 * q + i)) * 16) = make_uint4(u[0], u[1], u[2], u[3]);
                         }
                     }
-                } else {
-                    const float scale = __uint_as_float((uint32_t)(127 - bnext) << 23);
-                    for (int i = 0; i < 16 * NB; ++i) {
-                        uint4 *at = (uint4 *)(vt + (size_t)(lane + 32 * i) * 16);
-                        uint32_t u[4] = {at->x, at->y, at->z, at->w};
-                        for (int k = 0; k < 4; ++k)
-                            u[k] = pack_f16x2(__uint_as_float(u[k] << 16) * scale, __uint_as_float(u[k] & 0xFFFF0000u) * scale);
-                        *at = make_uint4(u[0], u[1], u[2], u[3]);
+                } else {  // the same, and an infinity or NaN stays one
+#pragma unroll 1
+                    for (int i = 0; i < 64 * NB; ++i) {
+                        uint32_t *at = (uint32_t *)vt + lane + 32 * i;
+                        const uint32_t a = *at & 0x7FFF7FFFu, odd = __vcmpgeu2(a, 0x7F807F80u);
+                        const uint32_t h = ((__vmaxu2(a, low2) - low2) << 3) & ~odd;
+                        *at = h | (((a & 0x007F007Fu) << 3 | 0x7C007C00u) & odd) | (*at & 0x80008000u);
                     }
                 }
                 fence_async_smem();

@@ -418,6 +418,27 @@ def test_extend_values_that_grow_along_the_sequence(cuda_device, dtype):
     check_state(x, state, [None])
 
 
+@pytest.mark.parametrize("dtype,indexed", [("bf16", False), ("bf16", True), ("f32", False)])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("L,d,at", [(700, 64, 130), (700, 128, 699), (1300, 64, 0), (12, 64, 3)])
+def test_extend_a_value_that_is_not_finite_stays_in_its_column(cuda_device, dtype, indexed, bad, L, d, at):
+    """What the single-token step does: the other columns of S', z' and D are as ever."""
+    x = Problem(1, 2, L, d, 128, dtype, cuda_device, prior=5, seed=L + at)
+    x.v[:, :, at, 7] = bad
+    state = api.decode_extend(x.k, x.v, x.W, x.state, index=i32([np.arange(L)], cuda_device) if indexed else None)
+    status_ok()
+    S, z = x.gpu_state(state)
+    rest = [c for c in range(d) if c != 7]
+    for h in range(2):
+        S0, z0 = x.oracle_state(0, h)
+        v = x.head(x.v, 0, h)
+        v[at, 7] = 0.0
+        Sr, zr = speculative.decode_extend(S0, z0, x.head(x.k, 0, h), v, x.W64)
+        assert np.abs(S[0, h] - Sr)[:, rest].max() <= TOL * np.abs(Sr).max()
+        assert np.abs(z[0, h] - zr).max() <= TOL * np.abs(zr).max()
+        assert not np.isfinite(S[0, h][:, 7]).any()
+
+
 def test_extend_then_step_continues_the_sequence(cuda_device):
     """A prompt through decode_extend, then single tokens: the rows of the causal forward."""
     from oracle import favor
