@@ -8,8 +8,9 @@
 //                              tile's largest exponent lands in (2, 3] and raised where a later one's
 //                              passes 15 (fp16 holds 2^t below 2^16; its smallest step is 2^-24);
 //   acc += phi'^T V'           tcgen05 (M = 128, N = d, K = 64), fp16 operands: phi' = hi + lo, two fp16
-//                              values (22 bits), A from TMEM where they replace P; V' = V 2^-b, exact in
-//                              fp16 but for entries 2^-20 of the tile's largest and below (off by 2^-21 of it);
+//                              values (22 bits), A from TMEM where they replace P; V' = V 2^-b, b per value
+//                              column: exact in fp16 but for entries 2^-20 of the column's largest in this
+//                              tile and below (off by 2^-21 of it);
 //   S_r <- 2^(..) S_r + 2^b acc  in fp32, every kExtFlush tiles and before a tile that changes D_r or b:
 //                              the tensor core's own accumulation truncates; over 512 tokens that bias
 //                              stays near 2e-6, over a long run it would reach 1e-5.
@@ -46,8 +47,74 @@ struct ExtTc {
     static constexpr uint32_t T_P = 0, T_ACC = 128;  // TMEM columns: two tiles of P, the accumulator
     static constexpr size_t OFF_K = WT, OFF_V = OFF_K + NS * KT, OFF_KX = OFF_V + NS * KT, OFF_WX = OFF_KX + NS * KX,
                             OFF_D = OFF_WX + 4096, OFF_F = OFF_D + kExtRing * 128 * 4, OFF_MISC = OFF_F + 128 * 8,
-                            OFF_BAR = OFF_MISC + 4 * 6 * kExtRing, BYTES = OFF_BAR + 8 * (4 * NS + 2 + 2 + 2 + 4 + 5 + 4) + 8 + 1024;
+                            OFF_B = OFF_MISC + 4 * 6 * kExtRing, OFF_BAR = OFF_B + kExtRing * D * 2, BYTES = OFF_BAR + 8 * (4 * NS + 2 + 2 + 2 + 4 + 5 + 4) + 8 + 1024;
 };
+
+// Per-column maxima of |entries| over a 64 x 64 block of V (a warp; `at`: the block's chunk of this lane).
+// Chunk lane + 32 i is row lane / 8 + 4 i, columns 8 (L ^ 4 (i % 2)) and on, L = (lane % 8) ^ (lane / 8): the
+// chunks of odd i change places between lanes of L and L ^ 4, then the lanes of one L come together. Returned
+// are columns 8 L + 2 (lane / 8) and the next, as two bf16 patterns.
+__device__ __forceinline__ void ext_swap(uint32_t (&mx)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mx[k] = __shfl_xor_sync(0xffffffffu, mx[k], 4);
+}
+__device__ __forceinline__ uint32_t ext_reduce(const uint32_t (&mx)[4], int lane) {
+    const bool h = (lane & 16) != 0, o = (lane & 8) != 0;
+    const uint32_t s0 = __shfl_xor_sync(0xffffffffu, h ? mx[0] : mx[2], 18);
+    const uint32_t s1 = __shfl_xor_sync(0xffffffffu, h ? mx[1] : mx[3], 18);
+    const uint32_t a = __vmaxu2(h ? mx[2] : mx[0], s0), b = __vmaxu2(h ? mx[3] : mx[1], s1);
+    return __vmaxu2(o ? b : a, __shfl_xor_sync(0xffffffffu, o ? a : b, 9));
+}
+__device__ __forceinline__ uint32_t ext_column_max(const uint8_t *at, int lane) {
+    uint32_t mx[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {  // odd i, then even i
+        if (q == 2) ext_swap(mx);
+        const uint8_t *c = at + (8 * (q & 1) + (q < 2 ? 1 : 0)) * 512;
+        uint4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *(const uint4 *)(c + i * 1024);
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            mx[0] = __vimax3_u16x2(mx[0], x[i].x & 0x7FFF7FFFu, x[i + 1].x & 0x7FFF7FFFu);
+            mx[1] = __vimax3_u16x2(mx[1], x[i].y & 0x7FFF7FFFu, x[i + 1].y & 0x7FFF7FFFu);
+            mx[2] = __vimax3_u16x2(mx[2], x[i].z & 0x7FFF7FFFu, x[i + 1].z & 0x7FFF7FFFu);
+            mx[3] = __vimax3_u16x2(mx[3], x[i].w & 0x7FFF7FFFu, x[i + 1].w & 0x7FFF7FFFu);
+        }
+    }
+    return ext_reduce(mx, lane);
+}
+// The same over the finite entries alone, and the conversion of a tile with others (rare; out of line, so
+// that the instruction cache keeps the ordinary path).
+__device__ __noinline__ uint32_t ext_column_max_finite(const uint8_t *at, int lane) {
+    uint32_t mx[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {
+        if (i == 8) ext_swap(mx);
+        const uint4 x = *(const uint4 *)(at + (i < 8 ? 2 * i + 1 : 2 * i - 16) * 512);
+        const uint32_t u[4] = {x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu, x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = __vmaxu2(mx[k], u[k] & ~__vcmpgeu2(u[k], 0x7F807F80u));
+    }
+    return ext_reduce(mx, lane);
+}
+__device__ __noinline__ void ext_convert_odd(uint8_t *vt, const uint16_t *sb, int lane) {
+    const int L = (lane & 7) ^ (lane >> 3);
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {
+        uint4 *at = (uint4 *)(vt + (lane + 32 * i) * 16);
+        const uint4 x = *at, lw = *(const uint4 *)(sb + 8 * (L ^ (4 * (i & 1))));
+        uint32_t u[4] = {x.x, x.y, x.z, x.w};
+        const uint32_t low[4] = {lw.x, lw.y, lw.z, lw.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // an infinity or NaN stays one
+            const uint32_t a = u[k] & 0x7FFF7FFFu, odd = __vcmpgeu2(a, 0x7F807F80u);
+            const uint32_t h = ((__vmaxu2(a, low[k]) - low[k]) << 3) & ~odd;
+            u[k] = h | (((a & 0x007F007Fu) << 3 | 0x7C007C00u) & odd) | (u[k] & 0x80008000u);
+        }
+        *at = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+}
 
 template <int D>
 __global__ void __launch_bounds__(ExtTc<D>::THREADS, 2)
@@ -61,7 +128,8 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
     float *sD = (float *)(smem + C::OFF_D);       // [tile % kExtRing][128]: D_r
     float2 *sF = (float2 *)(smem + C::OFF_F);     // [128]: final factors of the run's and the old S'
     int *sRaise = (int *)(smem + C::OFF_MISC);    // [tile % kExtRing][warp]: some D_r of this warp's changes here
-    int *sScale = sRaise + 4 * kExtRing, *sB = sScale + kExtRing;  // [tile % kExtRing]: b changes here; b
+    int *sScale = sRaise + 4 * kExtRing;          // [tile % kExtRing][block]: some b of its 64 columns changes here
+    uint16_t *sB = (uint16_t *)(smem + C::OFF_B); // [tile % kExtRing][D]: (112 + b) 2^7, as a bf16 exponent
     uint64_t *bars = (uint64_t *)(smem + C::OFF_BAR);
     uint64_t *k_full = bars, *v_full = k_full + NS, *k_conv = v_full + NS, *v_conv = k_conv + NS;
     uint64_t *p_full = v_conv + NS, *phi_full = p_full + 2, *s_done = phi_full + 2, *d_full = s_done + 2;
@@ -86,7 +154,7 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             mbar_init(&k_full[s], 1);
             mbar_init(&v_full[s], 1);
             mbar_init(&k_conv[s], 64);
-            mbar_init(&v_conv[s], 32);
+            mbar_init(&v_conv[s], 32 * NB);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&p_full[s], 1);
@@ -94,7 +162,7 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             mbar_init(&s_done[s], 1);
         }
         for (int s = 0; s < 4; ++s) {
-            mbar_init(&d_full[s], 160);
+            mbar_init(&d_full[s], 128 + 32 * NB);
             mbar_init(&b_set[s], 32);
         }
         mbar_init(w_full, 1);
@@ -125,8 +193,8 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
     // whether S takes the accumulator before tile g adds to it (read after tile g's d_full, or its phi_full
     // and v_conv)
     auto flush_before = [&](int g) {
-        const int *r = sRaise + 4 * (g % kExtRing);
-        return g > 0 && ((g % kExtFlush) == 0 || sScale[g % kExtRing] != 0 || (r[0] | r[1] | r[2] | r[3]) != 0);
+        const int *r = sRaise + 4 * (g % kExtRing), *b = sScale + 2 * (g % kExtRing);
+        return g > 0 && ((g % kExtFlush) == 0 || b[0] != 0 || (NB == 2 && b[1] != 0) || (r[0] | r[1] | r[2] | r[3]) != 0);
     };
 
     auto load = [&](const CUtensorMap *map, uint8_t *buf, uint64_t *bar, int g) {
@@ -315,81 +383,58 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                 mbar_arrive(&k_conv[s]);
                 return true;
             };
-            // Warps 6 and 7 in turn, V tile g to fp16 at scale 2^-b: b follows the tiles' largest finite magnitude (which lands in
-            // [2^12, 2^13)) only where it would leave [2^6, 2^15). A bf16 value's fp16 form at that scale is
-            // integer arithmetic on its bits, exact from 2^-14 on (smaller ones are off by 2^-15 at most).
+            // V tile g to fp16 at scale 2^-b, by warps 6 and 7 in turn or (d = 128) a block of 64 columns each: a
+            // column's b follows its largest finite magnitude in the tile (which lands in [2^12, 2^13)), all of
+            // a block where one would leave [2^6, 2^15). A bf16 value's fp16 form at that scale is integer
+            // arithmetic on its bits, exact from 2^-14 on (smaller ones are off by 2^-15 at most); infinities and
+            // NaN stay what they are.
             auto conv_v = [&](int g) -> bool {
-                const int s = g % NS;
+                const int s = g % NS, blk = NB == 2 ? warp & 1 : 0, L = (lane & 7) ^ (lane >> 3);
                 if (!mbar_wait_all(&v_full[s], (g / NS) & 1, abort_flag)) return false;
-                uint8_t *vt = sV + (size_t)s * C::KT;
+                uint8_t *vt = sV + (size_t)s * C::KT + blk * C::BLK;
+                uint16_t *sb = sB + (g % kExtRing) * D + 64 * blk;
                 const int valid = count - (t0 + g) * kExtTile;
-                // (16-byte chunks lane, lane + 32, ..: row (c / 8) % 64; four loads before what uses them)
                 if (valid < kExtTile)
-                    for (int c = lane; c < 512 * NB; c += 32)
-                        if ((c >> 3) % kExtTile >= valid) *(uint4 *)(vt + (size_t)c * 16) = make_uint4(0u, 0u, 0u, 0u);
-                uint32_t mx = 0;
-#pragma unroll 1
-                for (int q = 0; q < 4 * NB; ++q) {
-                    uint4 x[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[i] = *(const uint4 *)(vt + (size_t)(lane + 32 * (4 * q + i)) * 16);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t a = __vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu);
-                        const uint32_t b = __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu);
-                        mx = __vmaxu2(mx, __vmaxu2(a, b));
-                    }
-                }
-                mx = __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
-                const bool finite = mx < 0x7F80u;
-                if (!finite) {  // the other entries' largest: infinities and NaN concern their own columns only
-                    mx = 0;
-#pragma unroll 1
-                    for (int i = 0; i < 64 * NB; ++i) {
-                        const uint32_t a = ((const uint32_t *)vt)[lane + 32 * i] & 0x7FFF7FFFu;
-                        mx = __vmaxu2(mx, a & ~__vcmpgeu2(a, 0x7F807F80u));
-                    }
-                    mx = __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
-                }
-                int bnext = 0;  // b of the tile before, then of this one
-                if (g > 0) {
-                    if (!mbar_wait_all(&b_set[(g - 1) & 3], ((g - 1) >> 2) & 1, abort_flag)) return false;
-                    bnext = sB[(g - 1) % kExtRing];
-                }
-                const int b = min(max((int)(mx >> 7) - 127 - 12, -100), 114);
-                const bool changed = g == 0 || (mx != 0 && (b > bnext + 2 || b < bnext - 6));
-                if (changed) bnext = b;
-                if (lane == 0) {
-                    sScale[g % kExtRing] = changed;
-                    sB[g % kExtRing] = bnext;
+                    for (int c = lane; c < 512; c += 32)
+                        if ((c >> 3) >= valid) *(uint4 *)(vt + (size_t)c * 16) = make_uint4(0u, 0u, 0u, 0u);
+                uint32_t now = ext_column_max(vt + lane * 16, lane);  // of columns 8 L + 2 (lane / 8) and the next
+                const bool odd = __any_sync(0xffffffffu, max(now & 0xFFFFu, now >> 16) >= 0x7F80u);
+                if (odd) now = ext_column_max_finite(vt + lane * 16, lane);
+                // b from the exponent, within -100 .. 114; 0 where the column is
+                now = __vminu2(__vmaxu2(now & 0x7F807F80u, 0x13801380u) - 0x0D800D80u, 0x71007100u) & ~__vcmpeq2(now, 0u);
+                if (NB == 1 && g > 0 && !mbar_wait_all(&b_set[(g - 1) & 3], ((g - 1) >> 2) & 1, abort_flag)) return false;
+                {
+                    const int at = 4 * L + (lane >> 3);
+                    const uint32_t was = g > 0 ? ((const uint32_t *)(sB + ((g - 1) % kExtRing) * D + 64 * blk))[at] : 0x06000600u;
+                    now |= was & __vcmpeq2(now, 0u);
+                    const uint32_t by = now - was + 0x83008300u;  // b's change, from -6 to 2 or out of range
+                    const bool changed = __any_sync(0xffffffffu, by != __vmaxu2(__vminu2(by, 0x84008400u), 0x80008000u)) || g == 0;
+                    ((uint32_t *)sb)[at] = changed ? now : was;
+                    if (lane == 0) sScale[2 * (g % kExtRing) + blk] = changed;
                 }
                 __syncwarp();
-                mbar_arrive(&b_set[g & 3]);
+                if (NB == 1) mbar_arrive(&b_set[g & 3]);
                 mbar_arrive(&d_full[g & 3]);
-                const uint32_t low = (uint32_t)(112 + bnext) << 7, low2 = low | (low << 16);
-                if (finite) {
+                if (!odd) {
 #pragma unroll 1
-                    for (int q = 0; q < 4 * NB; ++q) {
+                    for (int q = 0; q < 4; ++q) {
+                        uint8_t *at = vt + lane * 16 + (8 * (q & 1) + (q >> 1)) * 512;
+                        const uint4 lw = *(const uint4 *)(sb + 8 * (L ^ (2 * (q & 2))));
+                        const uint32_t low[4] = {lw.x, lw.y, lw.z, lw.w};
                         uint4 x[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) x[i] = *(const uint4 *)(vt + (size_t)(lane + 32 * (4 * q + i)) * 16);
+                        for (int i = 0; i < 4; ++i) x[i] = *(const uint4 *)(at + i * 1024);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                u[k] = ((__vmaxu2(u[k] & 0x7FFF7FFFu, low2) - low2) << 3) | (u[k] & 0x80008000u);
-                            *(uint4 *)(vt + (size_t)(lane + 32 * (4 * q + i)) * 16) = make_uint4(u[0], u[1], u[2], u[3]);
+                                u[k] = ((__vmaxu2(u[k] & 0x7FFF7FFFu, low[k]) - low[k]) << 3) | (u[k] & 0x80008000u);
+                            *(uint4 *)(at + i * 1024) = make_uint4(u[0], u[1], u[2], u[3]);
                         }
                     }
-                } else {  // the same, and an infinity or NaN stays one
-#pragma unroll 1
-                    for (int i = 0; i < 64 * NB; ++i) {
-                        uint32_t *at = (uint32_t *)vt + lane + 32 * i;
-                        const uint32_t a = *at & 0x7FFF7FFFu, odd = __vcmpgeu2(a, 0x7F807F80u);
-                        const uint32_t h = ((__vmaxu2(a, low2) - low2) << 3) & ~odd;
-                        *at = h | (((a & 0x007F007Fu) << 3 | 0x7C007C00u) & odd) | (*at & 0x80008000u);
-                    }
+                } else {
+                    ext_convert_odd(vt, sb, lane);
                 }
                 fence_async_smem();
                 mbar_arrive(&v_conv[s]);
@@ -400,26 +445,46 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             // as local memory they took 33,000 cycles a flush)
             constexpr int SR = D == 64 ? D : 1;
             float S[SR];
-            float Dreg = 0.f, Dacc = 0.f;  // Dacc, bcur: the accumulator's D_r and b
-            int bcur = 0;
+            float Dreg = 0.f, Dacc = 0.f;  // Dacc: the accumulator's D_r
             bool first = true;
 #pragma unroll
             for (int c = 0; c < SR; ++c) S[c] = 0.f;
-            auto flush = [&]() {
+            auto flush = [&](int last) {  // the accumulator's last tile (its b is that of all of them)
                 const float keep = exp2f(fminf(Dreg - Dacc, 0.f));
-                const float up = __uint_as_float((uint32_t)(127 + bcur) << 23);
+                const uint16_t *sb = sB + (last % kExtRing) * D;
                 Dreg = Dacc;
                 float v[16];
+                // 16 columns times 2^b
+                auto scaled = [&](int q) {
+                    tmem_ld16(tL + C::T_ACC + q, v);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 x = *(const uint4 *)(sb + q + 8 * h);
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            v[8 * h + 2 * c] *= __uint_as_float((w[c] << 16) + 0x07800000u);
+                            v[8 * h + 2 * c + 1] *= __uint_as_float((w[c] & 0xFFFF0000u) + 0x07800000u);
+                        }
+                    }
+                };
                 if constexpr (D == 64) {
+                    // (in place and in a rolled loop: next to S there are no registers for the scales)
+#pragma unroll 1
+                    for (int q = 0; q < D; q += 16) {
+                        scaled(q);
+                        uint32_t u[16];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) u[c] = __float_as_uint(v[c]);
+                        tmem_st16u(tL + C::T_ACC + q, u);
+                    }
+                    tmem_wait_st();
 #pragma unroll
                     for (int q = 0; q < D; q += 16) {
                         tmem_ld16(tL + C::T_ACC + q, v);
 #pragma unroll
-                        for (int c = 0; c < 16; c += 2) {
-                            float a, b;
-                            ffma2(v[c], v[c + 1], up, up, 0.f, 0.f, a, b);
-                            ffma2(S[q + c], S[q + c + 1], keep, keep, a, b, S[q + c], S[q + c + 1]);
-                        }
+                        for (int c = 0; c < 16; c += 2)
+                            ffma2(S[q + c], S[q + c + 1], keep, keep, v[c], v[c + 1], S[q + c], S[q + c + 1]);
                     }
                 } else {
                     float *at = dst + r, s[16];
@@ -427,10 +492,10 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
                     for (int q = 0; q < D; q += 16, at += 16 * (size_t)m) {
 #pragma unroll
                         for (int c = 0; c < 16; ++c) s[c] = first || r >= m ? 0.f : __ldcg(at + (size_t)c * m);
-                        tmem_ld16(tL + C::T_ACC + q, v);
+                        scaled(q);
                         if (r < m) {
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) __stcg(at + (size_t)c * m, fmaf(s[c], keep, up * v[c]));
+                            for (int c = 0; c < 16; ++c) __stcg(at + (size_t)c * m, fmaf(s[c], keep, v[c]));
                         }
                     }
                     first = false;
@@ -440,31 +505,30 @@ k_decode_extend_tc(const __grid_constant__ CUtensorMap mapK, const __grid_consta
             };
             const bool keys = warp < 6;
             int flushes = 0;
-            // V is converted two tiles ahead, each tile by one of its warps, where there are slots for it
+            // V is converted two tiles ahead where there are slots for it, by one of its warps a tile; where there
+            // are not, that would be what everyone waits for (d = 128: 123 us for 16384 tokens in 16 heads, 118
+            // with half a tile each)
             constexpr int lead = NS >= 4 ? 2 : 1;
-            ok = keys ? conv_k(0) && (n < 2 || conv_k(1)) : (warp & 1) == 0 ? conv_v(0) : lead == 1 || n < 2 || conv_v(1);
+            auto mine = [&](int g) { return NB == 2 || (g & 1) == (warp & 1); };
+            ok = keys ? conv_k(0) && (n < 2 || conv_k(1)) : mine(0) ? conv_v(0) : lead == 1 || n < 2 || conv_v(1);
             for (int g = 0; ok && g < n; ++g) {
                 if (keys)
                     ok = g + 2 >= n || conv_k(g + 2);
                 else
-                    ok = g + lead >= n || ((g + lead) & 1) != (warp & 1) || conv_v(g + lead);
+                    ok = g + lead >= n || !mine(g + lead) || conv_v(g + lead);
                 if (!ok || !(ok = mbar_wait_all(&d_full[g & 3], (g >> 2) & 1, abort_flag))) break;
                 const bool take = flush_before(g);
                 const float Dg = sD[(g % kExtRing) * 128 + row];  // (before the accumulator is given back)
-                const int bg = sB[g % kExtRing];
                 if (take) {
                     if (!(ok = mbar_wait_all(acc_full, flushes++ & 1, abort_flag))) break;
                     tc_fence_after();
-                    flush();
+                    flush(g - 1);
                 }
-                if (take || g == 0) {
-                    Dacc = Dg;
-                    bcur = bg;
-                }
+                if (take || g == 0) Dacc = Dg;
             }
             if (ok && (ok = mbar_wait_all(acc_full, flushes & 1, abort_flag))) {
                 tc_fence_after();
-                flush();
+                flush(n - 1);
             }
             named_bar_sync(2, 256);
             // the run's S' in the state's units, joined with the carried one

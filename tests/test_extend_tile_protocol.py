@@ -30,7 +30,7 @@ def source_constants(d):
 class Walk:
     """Events in program order per warp; a barrier's phase completes after all its arrivals."""
 
-    def __init__(self, stages, lead, flush):
+    def __init__(self, d, stages, lead, flush):
         self.before = []       # per event: the events it directly follows
         self.at = {}           # warp -> its last event
         self.arrivals = {}     # (barrier, phase) -> arriving events
@@ -38,6 +38,9 @@ class Walk:
         self.touched = []      # (event, ring, tile, "r" or "w")
         self.flush = flush     # tiles the accumulator is taken before
         n, NS = TILES, stages
+        self.blocks = d // 64
+        self.scales = ("sScale6", "sScale7") if self.blocks == 2 else ("sScale",)
+        self.bs = ("sB6", "sB7") if self.blocks == 2 else ("sB",)
         self.E(n)
         for w in (4, 5):
             self.keys(w, n, NS)
@@ -72,11 +75,13 @@ class Walk:
 
     def take(self, warp, g):  # what warps 4-7 do at tile g
         self.wait(warp, ("d_full", g & 3), g >> 2)
-        for ring in ("sRaise", "sScale", "sD", "sB"):
+        for ring in ("sRaise", "sD") + self.scales:
             self.touch(warp, ring, g, "r")
         if g in self.flush:
             k = sorted(self.flush).index(g)
             self.wait(warp, ("acc_full", 0), k)
+            for ring in self.bs:
+                self.touch(warp, ring, g - 1, "r")
             self.arrive(warp, ("acc_free", 0), k)
 
     def keys(self, w, n, NS):
@@ -92,22 +97,30 @@ class Walk:
             self.take(w, g)
 
     def values(self, w, n, lead, NS):
+        halves = self.blocks == 2  # each warp takes its half of every tile, else every second tile
+        scale, b = (f"sScale{w}", f"sB{w}") if halves else ("sScale", "sB")
+
+        def mine(g):
+            return halves or (g & 1) == (w & 1)
+
         def conv(g):
             self.wait(w, ("v_full", g % NS), g // NS)
             if g > 0:
-                self.wait(w, ("b_set", (g - 1) & 3), (g - 1) >> 2)
-                self.touch(w, "sB", g - 1, "r")
-            self.touch(w, "sScale", g, "w")
-            self.touch(w, "sB", g, "w")
-            self.arrive(w, ("b_set", g & 3), g >> 2)
+                if not halves:
+                    self.wait(w, ("b_set", (g - 1) & 3), (g - 1) >> 2)
+                self.touch(w, b, g - 1, "r")
+            self.touch(w, b, g, "w")
+            self.touch(w, scale, g, "w")
+            if not halves:
+                self.arrive(w, ("b_set", g & 3), g >> 2)
             self.arrive(w, ("d_full", g & 3), g >> 2)
             self.arrive(w, ("v_conv", g % NS), g // NS)
 
         for g in range(lead):
-            if (g & 1) == (w & 1):
+            if mine(g):
                 conv(g)
         for g in range(n):
-            if g + lead < n and ((g + lead) & 1) == (w & 1):
+            if g + lead < n and mine(g + lead):
                 conv(g + lead)
             self.take(w, g)
 
@@ -144,7 +157,8 @@ class Walk:
             self.wait(9, ("v_conv", j % NS), j // NS)
             self.wait(9, ("phi_full", j & 1), j >> 1)
             self.touch(9, "sRaise", j, "r")
-            self.touch(9, "sScale", j, "r")
+            for ring in self.scales:
+                self.touch(9, ring, j, "r")
             if j in self.flush:
                 self.arrive(9, ("acc_full", 0), taken)
                 self.wait(9, ("acc_free", 0), taken)
@@ -206,15 +220,13 @@ FLUSHES = [set(), {16, 32}, set(range(1, TILES)), {3, 4, 5, 16, 17, 32}] + \
 @pytest.mark.parametrize("d", [64, 128])
 def test_ring_entries_are_read_before_they_are_written_again(d, flush):
     ring, stages, lead = source_constants(d)
-    walk = Walk(stages, lead, flush)
+    walk = Walk(d, stages, lead, flush)
     assert not walk.overwritten(ring)
     assert not walk.overrun()
 
 
-@pytest.mark.parametrize("d", [64, 128])
-def test_four_entries_would_not_do(d):
+def test_four_entries_would_not_do():
     """The walk sees the fault that rings of four tiles had: between flushes the exponent warps come round
     to a tile's entry while a value warp still has to read it."""
-    _, stages, lead = source_constants(d)
-    bad = Walk(stages, lead, set()).overwritten(4)
+    bad = Walk(64, 4, 2, set()).overwritten(4)
     assert {name for name, _ in bad} >= {"sD", "sRaise"}

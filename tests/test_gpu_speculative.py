@@ -418,6 +418,27 @@ def test_extend_values_that_grow_along_the_sequence(cuda_device, dtype):
     check_state(x, state, [None])
 
 
+def column_scales(d, lowest, device):
+    """Powers of two from 1 down to 2^lowest, one per value column, neighbours far apart (exact in any type)."""
+    e = torch.round(torch.linspace(0, lowest, d))[torch.randperm(d, generator=torch.Generator().manual_seed(d))]
+    return torch.exp2(e).to(device)
+
+
+@pytest.mark.parametrize("dtype,indexed", [("bf16", False), ("bf16", True), ("f32", False)])
+@pytest.mark.parametrize("lowest", [-20, -60])
+@pytest.mark.parametrize("L,d,m", [(64, 64, 256), (700, 64, 128), (700, 128, 128), (2500, 64, 96), (13, 128, 256)])
+def test_extend_value_columns_of_very_different_size(cuda_device, dtype, indexed, lowest, L, d, m):
+    """Each column of S' to the tolerance of its own largest entry."""
+    x = Problem(1, 2, L, d, m, dtype, cuda_device, prior=0, seed=L + d)
+    x.v *= column_scales(d, lowest, cuda_device).to(x.v.dtype)
+    state = api.decode_extend(x.k, x.v, x.W, x.state, index=i32([np.arange(L)], cuda_device) if indexed else None)
+    status_ok()
+    S, z = x.gpu_state(state)
+    for h in range(2):
+        Sr, zr = speculative.decode_extend(np.zeros((m, d)), np.zeros(m), x.head(x.k, 0, h), x.head(x.v, 0, h), x.W64)
+        assert (np.abs(S[0, h] - Sr).max(0) <= TOL * np.abs(Sr).max(0)).all()
+
+
 @pytest.mark.parametrize("dtype,indexed", [("bf16", False), ("bf16", True), ("f32", False)])
 @pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
 @pytest.mark.parametrize("L,d,at", [(700, 64, 130), (700, 128, 699), (1300, 64, 0), (12, 64, 3)])
