@@ -205,9 +205,24 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else None
 
 
-def _alloc_bytes(n, device):
+def _empty(size, dtype, device, stream, returned=True):
+    """A tensor for a call on ``stream`` (None: the current one). It comes from that stream's memory: a block
+    just freed on another may still be in use there, by work this stream does not wait for. One that is
+    returned is used on the current stream next, so it must not be handed out before that is done with it."""
     torch = _torch()
-    return torch.empty(max(int(n), 256), dtype=torch.uint8, device=device)
+    if stream is None:
+        return torch.empty(size, dtype=dtype, device=device)
+    if stream.device != device:
+        raise FavorError(FAVOR_ERR_INVALID_ARG, f"stream is on {stream.device}, the tensors are on {device}")
+    with torch.cuda.stream(stream):
+        t = torch.empty(size, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _alloc_bytes(n, device, stream=None):
+    return _empty(max(int(n), 256), _torch().uint8, device, stream, returned=False)
 
 
 def _check_inputs(tensors, dtype_like):
@@ -225,12 +240,12 @@ def fwd(Q, K, V, W, causal=False, out=None, ctx=None, workspace=None, opts=None,
     _check_inputs((Q, K, V, W), Q)
     shape = _shape_of(Q, W)
     if out is None:
-        out = torch.empty(Q.shape, dtype=torch.float32, device=Q.device)
+        out = _empty(Q.shape, torch.float32, Q.device, stream)
     if workspace is None:
         ws_n = workspace_size(shape, causal, False, opts)
         if ws_n == 0:
             raise FavorError(FAVOR_ERR_UNSUPPORTED, "favor_workspace_size")
-        workspace = _alloc_bytes(ws_n, Q.device)
+        workspace = _alloc_bytes(ws_n, Q.device, stream)
     st = library().favor_fwd(ctypes.byref(shape), _ptr(Q), _ptr(K), _ptr(V), _ptr(W), int(causal), _ptr(out),
                              _ptr(ctx), _ptr(workspace), workspace.numel(),
                              ctypes.byref(opts) if opts is not None else None, _stream_ptr(stream))
@@ -243,12 +258,12 @@ def bwd(Q, K, V, W, out, dout, ctx=None, causal=False, workspace=None, opts=None
     torch = _torch()
     _check_inputs((Q, K, V, W, dout), Q)
     shape = _shape_of(Q, W)
-    dQ, dK, dV = (torch.empty(Q.shape, dtype=torch.float32, device=Q.device) for _ in range(3))
+    dQ, dK, dV = (_empty(Q.shape, torch.float32, Q.device, stream) for _ in range(3))
     if workspace is None:
         ws_n = workspace_size(shape, causal, True, opts)
         if ws_n == 0:
             raise FavorError(FAVOR_ERR_UNSUPPORTED, "favor_workspace_size")
-        workspace = _alloc_bytes(ws_n, Q.device)
+        workspace = _alloc_bytes(ws_n, Q.device, stream)
     st = library().favor_bwd(ctypes.byref(shape), _ptr(Q), _ptr(K), _ptr(V), _ptr(W), _ptr(out), _ptr(dout),
                              _ptr(ctx), int(causal), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(workspace),
                              workspace.numel(), ctypes.byref(opts) if opts is not None else None,
@@ -266,7 +281,7 @@ def bwd_into(Q, K, V, W, out, dout, dQ, dK, dV, ctx=None, causal=False, workspac
         ws_n = workspace_size(shape, causal, True, opts)
         if ws_n == 0:
             raise FavorError(FAVOR_ERR_UNSUPPORTED, "favor_workspace_size")
-        workspace = _alloc_bytes(ws_n, Q.device)
+        workspace = _alloc_bytes(ws_n, Q.device, stream)
     st = library().favor_bwd(ctypes.byref(shape), _ptr(Q), _ptr(K), _ptr(V), _ptr(W), _ptr(out), _ptr(dout),
                              _ptr(ctx), int(causal), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(workspace),
                              workspace.numel(), ctypes.byref(opts) if opts is not None else None,
@@ -287,9 +302,9 @@ def sp_state(K, V, W, state=None, workspace=None, stream=None):
     shape = _shape_of(K, W)
     lib = library()
     if state is None:
-        state = torch.empty(lib.favor_sp_state_size(ctypes.byref(shape)) // 4, dtype=torch.float32, device=K.device)
+        state = _empty(lib.favor_sp_state_size(ctypes.byref(shape)) // 4, torch.float32, K.device, stream)
     if workspace is None:
-        workspace = _alloc_bytes(lib.favor_sp_workspace_size(ctypes.byref(shape)), K.device)
+        workspace = _alloc_bytes(lib.favor_sp_workspace_size(ctypes.byref(shape)), K.device, stream)
     st = lib.favor_sp_state(ctypes.byref(shape), _ptr(K), _ptr(V), _ptr(W), _ptr(state), _ptr(workspace),
                             workspace.numel(), _stream_ptr(stream))
     _check(st, "favor_sp_state")
@@ -303,9 +318,9 @@ def sp_output(Q, W, state, out=None, workspace=None, stream=None):
     shape = _shape_of(Q, W)
     lib = library()
     if out is None:
-        out = torch.empty(Q.shape, dtype=torch.float32, device=Q.device)
+        out = _empty(Q.shape, torch.float32, Q.device, stream)
     if workspace is None:
-        workspace = _alloc_bytes(lib.favor_sp_workspace_size(ctypes.byref(shape)), Q.device)
+        workspace = _alloc_bytes(lib.favor_sp_workspace_size(ctypes.byref(shape)), Q.device, stream)
     st = lib.favor_sp_output(ctypes.byref(shape), _ptr(Q), _ptr(W), _ptr(state), _ptr(out), _ptr(workspace),
                              workspace.numel(), _stream_ptr(stream))
     _check(st, "favor_sp_output")
@@ -342,7 +357,7 @@ def decode_step(q, k, v, W, state, out=None, stream=None):
     B, H, d = q.shape
     shape = make_shape(B, H, 1, d, W.shape[0], _dtype_code(q))
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+        out = _empty(q.shape, torch.float32, q.device, stream)
     st = library().favor_decode_step(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(W), _ptr(state),
                                      _ptr(out), _stream_ptr(stream))
     _check(st, "favor_decode_step")
@@ -392,16 +407,11 @@ def _tokens(first, rest, W, state):
     return (B, H, L, d, m, _dtype_code(first)), device
 
 
-def _launch(what, f, device, stream, own, *args):
+def _launch(what, f, device, stream, *args):
     """Calls an entry point whose last argument is the stream (default: the current one of the tensors'
-    device) with that device current. ``own``: tensors allocated for the call on the current stream; one
-    that another stream uses must not be handed out again before that stream is done with it."""
+    device) with that device current."""
     torch = _torch()
-    current = torch._C._cuda_getCurrentRawStream(device.index)
-    raw = current if stream is None else stream.cuda_stream
-    if raw != current:
-        for t in own:
-            t.record_stream(stream)
+    raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
     if torch._C._cuda_getDevice() == device.index:
         st = f(*args, raw)
     else:
@@ -422,13 +432,11 @@ def decode_tree(q, k, v, W, state, parents, n_nodes=None, out=None, stream=None)
     i32 = torch.int32
     _fits("parents", parents, (dims[0], dims[2]), i32, device)
     nodes = _opt_ptr("n_nodes", n_nodes, (dims[0],), i32, device)
-    own = ()
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float32, device=device)
-        own = (out,)
+        out = _empty(q.shape, torch.float32, device, stream)
     else:
         _fits("out", out, q.shape, torch.float32, device)
-    _launch("favor_decode_tree", library().favor_decode_tree, device, stream, own, _shape_ref(Shape, *dims), q.data_ptr(),
+    _launch("favor_decode_tree", library().favor_decode_tree, device, stream, _shape_ref(Shape, *dims), q.data_ptr(),
             k.data_ptr(), v.data_ptr(), W.data_ptr(), state.data_ptr(), parents.data_ptr(), nodes, out.data_ptr())
     return out
 
@@ -453,14 +461,13 @@ def decode_extend(k, v, W, state, index=None, counts=None, workspace=None, strea
         n_index = index.shape[1]
         _fits("index", index, (dims[0], n_index), i32, device)
         index_ptr = index.data_ptr()
-    n_tok, own = _opt_ptr("counts", counts, (dims[0],), i32, device), ()
+    n_tok = _opt_ptr("counts", counts, (dims[0],), i32, device)
     if workspace is None:
         ws_n = _extend_workspace(device.index, n_index, *dims)
         if ws_n == 0:
             raise FavorError(FAVOR_ERR_UNSUPPORTED, "favor_decode_extend_workspace_size")
-        workspace = torch.empty(ws_n, dtype=torch.uint8, device=device)
-        own = (workspace,)
-    _launch("favor_decode_extend", library().favor_decode_extend, device, stream, own, _shape_ref(Shape, *dims),
+        workspace = _empty(ws_n, torch.uint8, device, stream, returned=False)
+    _launch("favor_decode_extend", library().favor_decode_extend, device, stream, _shape_ref(Shape, *dims),
             k.data_ptr(), v.data_ptr(), W.data_ptr(), index_ptr, n_index, n_tok, state.data_ptr(),
             workspace.data_ptr(), workspace.numel())
     return state
@@ -484,8 +491,11 @@ def decode_verify(parents, tokens, p, u, r, q=None, n_nodes=None, stream=None):
     used = _opt_ptr("n_nodes", n_nodes, row, i32, device)
     _fits("u", u, nodes, f32, device)
     _fits("r", r, row, f32, device)
-    path, n_path, token = parents.new_empty(nodes), parents.new_empty(row), parents.new_empty(row)
-    _launch("favor_decode_verify", library().favor_decode_verify, device, stream, (path, n_path, token),
+    if stream is None:
+        path, n_path, token = parents.new_empty(nodes), parents.new_empty(row), parents.new_empty(row)
+    else:
+        path, n_path, token = (_empty(size, i32, device, stream) for size in (nodes, row, row))
+    _launch("favor_decode_verify", library().favor_decode_verify, device, stream,
             _shape_ref(VerifyShape, B, T, V, _dtype_code(p)), parents.data_ptr(), tokens.data_ptr(), used, p.data_ptr(),
             draft, u.data_ptr(), r.data_ptr(), path.data_ptr(), n_path.data_ptr(), token.data_ptr())
     return path, n_path, token
@@ -507,7 +517,7 @@ def fwd_static_scratch(Q, K, V, W, out=None, stream=None):
     _check_inputs((Q, K, V, W), Q)
     shape = _shape_of(Q, W)
     if out is None:
-        out = torch.empty(Q.shape, dtype=torch.float32, device=Q.device)
+        out = _empty(Q.shape, torch.float32, Q.device, stream)
     st = library().favor_fwd_static_scratch(ctypes.byref(shape), _ptr(Q), _ptr(K), _ptr(V), _ptr(W), _ptr(out),
                                             _stream_ptr(stream))
     _check(st, "favor_fwd_static_scratch")

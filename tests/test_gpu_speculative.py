@@ -716,6 +716,47 @@ def test_calls_given_a_stream(cuda_device):
     status_ok()
 
 
+def test_calls_given_a_stream_leave_memory_in_use_alone(cuda_device):
+    """A block freed on the current stream, whose queued work still reads or writes it, is not what a call on
+    another stream takes for its workspace or results."""
+    x = Problem(1, 4, 4000, 64, 256, "bf16", cuda_device, prior=0, seed=62)
+    y = draft(4, 20, 20000, "f32", cuda_device, seed=63)
+    parents, tokens = i32(y["parents"], cuda_device), i32(y["tokens"], cuda_device)
+    u, r = (torch.tensor(y[k], device=cuda_device) for k in "ur")
+    t = [z[:, :, :40].contiguous() for z in (x.q, x.k, x.v)]
+    tree = i32(random_parents(1, 40), cuda_device)
+    state = api.decode_extend(x.k, x.v, x.W, x.state.clone())
+    n = api.library().favor_decode_extend_workspace_size(api.ctypes.byref(api.make_shape(1, 4, 4000, 64, 256, api.FAVOR_BF16)), 0)
+    short = [z[:, :, :300].contiguous() for z in (x.q, x.k, x.v)]
+    one = [z[:, :, 0].contiguous() for z in t]
+    sizes = {"extend": n, "tree": 4 * t[0].numel(), "verify": 4 * parents.numel(), "fwd": 4 * short[0].numel(),
+             "step": 4 * one[0].numel()}
+    calls = {"extend": lambda s, st: (api.decode_extend(x.k, x.v, x.W, st, stream=s),),
+             "tree": lambda s, st: (api.decode_tree(*t, x.W, st, tree, stream=s),),
+             "verify": lambda s, st: api.decode_verify(parents, tokens, y["p"], u, r, q=y["q"], stream=s),
+             "fwd": lambda s, st: (api.fwd(*short, x.W, stream=s),),
+             "step": lambda s, st: (api.decode_step(*one, x.W, st, stream=s),)}
+    side = torch.cuda.Stream()
+    for name, call in calls.items():
+        start = x.state if name == "extend" else state
+        want = [z.clone() for z in call(None, start.clone())]
+        for _ in range(2):
+            mine = start.clone()
+            torch.cuda.synchronize()
+            block = torch.full((sizes[name],), 7, dtype=torch.uint8, device=cuda_device)
+            torch.cuda.synchronize()
+            torch.cuda._sleep(20000000)
+            seen = block.clone()
+            block.fill_(255)
+            del block
+            got = call(side, mine)
+            side.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+            torch.cuda.synchronize()
+            assert (seen == 7).all() and all(torch.equal(a, b) for a, b in zip(got, want)), name
+    status_ok()
+
+
 def test_binding_refuses_what_does_not_fit(cuda_device):
     x = Problem(2, 2, 6, 64, 128, "bf16", cuda_device, prior=0)
     parents = i32(random_parents(2, 6), cuda_device)
