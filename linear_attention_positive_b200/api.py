@@ -443,8 +443,9 @@ def decode_tree(q, k, v, W, state, parents, n_nodes=None, out=None, stream=None)
 
 @functools.lru_cache(maxsize=256)
 def _extend_workspace(device_index, n_index, *dims):
-    """favor_decode_extend_workspace_size of a shape (it depends on the device's SM count too)."""
-    return library().favor_decode_extend_workspace_size(_shape_ref(Shape, *dims), n_index)
+    """favor_decode_extend_workspace_size of a shape on a device (it depends on the SM count)."""
+    with _torch().cuda.device(device_index):
+        return library().favor_decode_extend_workspace_size(_shape_ref(Shape, *dims), n_index)
 
 
 def decode_extend(k, v, W, state, index=None, counts=None, workspace=None, stream=None):

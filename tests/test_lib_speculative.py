@@ -89,3 +89,33 @@ def test_binding_refuses_host_tensors(favor_lib):
         with pytest.raises(api.FavorError) as e:
             call()
         assert e.value.status == INVALID
+
+
+def test_extend_workspace_is_asked_for_on_the_tensors_device(favor_lib, monkeypatch):
+    """The size follows the SM count of the current device, so it is asked for with the tensors' device
+    current (stand-ins for the device switch and the library)."""
+    current = [0]
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *_):
+            current[0] = self.before
+
+    class Library:
+        @staticmethod
+        def favor_decode_extend_workspace_size(shape, n_index):
+            return 1000 + current[0]
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(api, "library", lambda: Library)
+    dims = (1, 16, 4096, 64, 256, api.FAVOR_BF16)
+    api._extend_workspace.cache_clear()
+    try:
+        assert [api._extend_workspace(i, 0, *dims) for i in (1, 0, 1)] == [1001, 1000, 1001]
+    finally:
+        api._extend_workspace.cache_clear()
