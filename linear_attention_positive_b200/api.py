@@ -225,6 +225,13 @@ def _alloc_bytes(n, device, stream=None):
     return _empty(max(int(n), 256), _torch().uint8, device, stream, returned=False)
 
 
+def _workspace_bytes(workspace, device):
+    """Bytes of a caller's workspace, which must be contiguous memory of the tensors' device."""
+    if workspace.device != device or not workspace.is_contiguous():
+        raise FavorError(FAVOR_ERR_INVALID_ARG, f"workspace must be a contiguous tensor on {device}")
+    return workspace.numel() * workspace.element_size()
+
+
 def _check_inputs(tensors, dtype_like):
     for t in tensors:
         if not t.is_cuda or not t.is_contiguous():
@@ -247,7 +254,7 @@ def fwd(Q, K, V, W, causal=False, out=None, ctx=None, workspace=None, opts=None,
             raise FavorError(FAVOR_ERR_UNSUPPORTED, "favor_workspace_size")
         workspace = _alloc_bytes(ws_n, Q.device, stream)
     st = library().favor_fwd(ctypes.byref(shape), _ptr(Q), _ptr(K), _ptr(V), _ptr(W), int(causal), _ptr(out),
-                             _ptr(ctx), _ptr(workspace), workspace.numel(),
+                             _ptr(ctx), _ptr(workspace), _workspace_bytes(workspace, Q.device),
                              ctypes.byref(opts) if opts is not None else None, _stream_ptr(stream))
     _check(st, "favor_fwd")
     return out
@@ -266,7 +273,7 @@ def bwd(Q, K, V, W, out, dout, ctx=None, causal=False, workspace=None, opts=None
         workspace = _alloc_bytes(ws_n, Q.device, stream)
     st = library().favor_bwd(ctypes.byref(shape), _ptr(Q), _ptr(K), _ptr(V), _ptr(W), _ptr(out), _ptr(dout),
                              _ptr(ctx), int(causal), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(workspace),
-                             workspace.numel(), ctypes.byref(opts) if opts is not None else None,
+                             _workspace_bytes(workspace, Q.device), ctypes.byref(opts) if opts is not None else None,
                              _stream_ptr(stream))
     _check(st, "favor_bwd")
     return dQ, dK, dV
@@ -284,7 +291,7 @@ def bwd_into(Q, K, V, W, out, dout, dQ, dK, dV, ctx=None, causal=False, workspac
         workspace = _alloc_bytes(ws_n, Q.device, stream)
     st = library().favor_bwd(ctypes.byref(shape), _ptr(Q), _ptr(K), _ptr(V), _ptr(W), _ptr(out), _ptr(dout),
                              _ptr(ctx), int(causal), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(workspace),
-                             workspace.numel(), ctypes.byref(opts) if opts is not None else None,
+                             _workspace_bytes(workspace, Q.device), ctypes.byref(opts) if opts is not None else None,
                              _stream_ptr(stream))
     _check(st, "favor_bwd")
     return dQ, dK, dV
@@ -306,7 +313,7 @@ def sp_state(K, V, W, state=None, workspace=None, stream=None):
     if workspace is None:
         workspace = _alloc_bytes(lib.favor_sp_workspace_size(ctypes.byref(shape)), K.device, stream)
     st = lib.favor_sp_state(ctypes.byref(shape), _ptr(K), _ptr(V), _ptr(W), _ptr(state), _ptr(workspace),
-                            workspace.numel(), _stream_ptr(stream))
+                            _workspace_bytes(workspace, K.device), _stream_ptr(stream))
     _check(st, "favor_sp_state")
     return state
 
@@ -322,7 +329,7 @@ def sp_output(Q, W, state, out=None, workspace=None, stream=None):
     if workspace is None:
         workspace = _alloc_bytes(lib.favor_sp_workspace_size(ctypes.byref(shape)), Q.device, stream)
     st = lib.favor_sp_output(ctypes.byref(shape), _ptr(Q), _ptr(W), _ptr(state), _ptr(out), _ptr(workspace),
-                             workspace.numel(), _stream_ptr(stream))
+                             _workspace_bytes(workspace, Q.device), _stream_ptr(stream))
     _check(st, "favor_sp_output")
     return out
 
@@ -470,7 +477,7 @@ def decode_extend(k, v, W, state, index=None, counts=None, workspace=None, strea
         workspace = _empty(ws_n, torch.uint8, device, stream, returned=False)
     _launch("favor_decode_extend", library().favor_decode_extend, device, stream, _shape_ref(Shape, *dims),
             k.data_ptr(), v.data_ptr(), W.data_ptr(), index_ptr, n_index, n_tok, state.data_ptr(),
-            workspace.data_ptr(), workspace.numel())
+            workspace.data_ptr(), _workspace_bytes(workspace, device))
     return state
 
 

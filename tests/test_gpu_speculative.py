@@ -787,3 +787,15 @@ def test_binding_refuses_what_does_not_fit(cuda_device):
             call()
         assert e.value.status == api.FAVOR_ERR_INVALID_ARG, i
     status_ok()
+
+
+def test_binding_refuses_a_workspace_of_the_host(cuda_device):
+    x = Problem(2, 2, 6, 64, 128, "bf16", cuda_device, prior=0)
+    ws = torch.empty(1 << 24, dtype=torch.uint8)
+    for call in (lambda: api.decode_extend(x.k, x.v, x.W, x.state, workspace=ws),
+                 lambda: api.fwd(x.q, x.k, x.v, x.W, workspace=ws),
+                 lambda: api.sp_state(x.k, x.v, x.W, workspace=ws)):
+        with pytest.raises(api.FavorError) as e:
+            call()
+        assert e.value.status == api.FAVOR_ERR_INVALID_ARG
+    status_ok()

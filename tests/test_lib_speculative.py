@@ -119,3 +119,14 @@ def test_extend_workspace_is_asked_for_on_the_tensors_device(favor_lib, monkeypa
         assert [api._extend_workspace(i, 0, *dims) for i in (1, 0, 1)] == [1001, 1000, 1001]
     finally:
         api._extend_workspace.cache_clear()
+
+
+def test_a_workspace_is_memory_of_the_tensors_device():
+    """Its size counts in bytes whatever its type; one of another device is refused before any call."""
+    cpu = torch.device("cpu")
+    assert api._workspace_bytes(torch.empty(300, dtype=torch.float32), cpu) == 1200
+    for bad, device in ((torch.empty(300), torch.device("cuda:0")), (torch.empty(300, device="meta"), cpu),
+                        (torch.empty(20, 30).t(), cpu)):
+        with pytest.raises(api.FavorError) as e:
+            api._workspace_bytes(bad, device)
+        assert e.value.status == INVALID
