@@ -294,7 +294,8 @@ FAVOR_API size_t favor_decode_extend_workspace_size(const favor_shape *shape, in
  * k, v, W, state 16-byte aligned, index and counts 4-byte. fp32 precision for either dtype, in each value
  * column relative to its own largest entries (bf16 tokens in order: entries below 2^-20 of their column's
  * largest among 64 tokens are off by up to 2^-21 of it); a value that is not finite makes its column of S'
- * so, and no other. The same inputs give the same bits. Errors as favor_decode_tree, and FAVOR_ERR_WORKSPACE.
+ * so, and no other. The same inputs give the same bits. Errors as favor_decode_tree (L or
+ * n_index above 2^30: FAVOR_ERR_UNSUPPORTED), and FAVOR_ERR_WORKSPACE.
  */
 FAVOR_API favor_status favor_decode_extend(const favor_shape *shape, const void *k, const void *v, const void *W,
                                            const int *index, int n_index, const int *counts, float *state,

@@ -1136,6 +1136,7 @@ bool tree_on_tiles(const favor_shape *s) {
 //   are cut so that the CTAs fill the SMs once (two to an SM up to 128 features).
 //   Tensor cores: as many runs of whole tiles as fill two CTAs an SM once (d = 128: kExtFlush tiles at most).
 constexpr int kExtTcMin = 64;
+constexpr int kExtMaxTokens = 1 << 30;  // (a run's end, one run past the last token, stays an int)
 struct ExtendPlan {
     bool tc;
     int n_split, tok_per_split;
@@ -1182,7 +1183,7 @@ extern "C" favor_status favor_decode_tree(const favor_shape *s, const void *q, c
 }
 
 extern "C" size_t favor_decode_extend_workspace_size(const favor_shape *s, int n_index) {
-    if (!shape_ok(s) || n_index < 0 || !decode_supported(s)) return 0;
+    if (!shape_ok(s) || n_index < 0 || n_index > kExtMaxTokens || s->L > kExtMaxTokens || !decode_supported(s)) return 0;
     const ExtendPlan pl = extend_plan(s, n_index > 0 ? n_index : s->L, n_index > 0);
     // (at d = 128 two CTAs of a head add their columns through a partial state, one run or not)
     if (pl.n_split == 1 && (s->d == 64 || (!pl.tc && pl.tok_per_split <= kExtPath))) return 256;
@@ -1197,7 +1198,7 @@ extern "C" favor_status favor_decode_extend(const favor_shape *s, const void *k,
     if ((index == nullptr) != (n_index == 0) || n_index < 0) return FAVOR_ERR_INVALID_ARG;
     if (!aligned16(k) || !aligned16(v) || !aligned16(W) || !aligned16(state) || !aligned4(index) || !aligned4(counts))
         return FAVOR_ERR_INVALID_ARG;
-    if (!decode_supported(s)) return FAVOR_ERR_UNSUPPORTED;
+    if (!decode_supported(s) || n_index > kExtMaxTokens || s->L > kExtMaxTokens) return FAVOR_ERR_UNSUPPORTED;
     if (workspace == nullptr || ((uintptr_t)workspace & 255u) != 0 ||
         ws_bytes < favor_decode_extend_workspace_size(s, n_index))
         return FAVOR_ERR_WORKSPACE;

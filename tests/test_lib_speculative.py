@@ -130,3 +130,15 @@ def test_a_workspace_is_memory_of_the_tensors_device():
         with pytest.raises(api.FavorError) as e:
             api._workspace_bytes(bad, device)
         assert e.value.status == INVALID
+
+
+def test_decode_extend_refuses_token_counts_whose_runs_would_pass_32_bits(favor_lib):
+    f, size, most = favor_lib.favor_decode_extend, favor_lib.favor_decode_extend_workspace_size, 1 << 30
+    for dtype in (api.FAVOR_F32, api.FAVOR_BF16):
+        few, many = shape(1, 1, 8, 64, 256, dtype), shape(1, 1, most + 1, 64, 256, dtype)
+        assert size(few, most) > 0
+        for n in (most + 1, 2**31 - 1):
+            assert size(few, n) == 0
+            assert f(few, P, P, P, P, n, P, P, P, 1 << 40, NULL) == UNSUPPORTED
+        assert size(many, 0) == 0
+        assert f(many, P, P, P, NULL, 0, P, P, P, 1 << 40, NULL) == UNSUPPORTED
