@@ -13,11 +13,11 @@
 //
 // Precision: a, b and s S' enter the MMAs as hi + lo, two fp16 values (22 bits), products hi hi,
 // hi lo, lo hi; a and b are scaled by 2^15, so that a term 2^-18 below its maximum keeps all 22 bits
-// and fp16's smallest step is an error of at most 2^-40 of the maximum. s S' is scaled by its first
-// 64 features' largest magnitude to about 2^6 (1000 times that still fits). Weights of values are three
-// bf16 parts against the bf16 values. The steps' error in a row is at most
+// and fp16's smallest step is an error of at most 2^-40 of the maximum. Each column of s S' is scaled by
+// its first 64 features' largest magnitude to about 2^6 (1000 times that still fits). Weights of values are
+// three bf16 parts against the bf16 values. The steps' error in a row is at most
 //   2^-40 sum_{j in J(i)} 2^G_j (sum_r a_jr + sum_r b_ir) + 2^-31 sum_r b_ir
-// (the second part: s S', at most 2^-25 2^-6 of its largest magnitude); a row where that bound exceeds
+// (the second part: s S', at most 2^-25 2^-6 of its column's largest magnitude); a row where that bound exceeds
 // 2^-14 of the denominator (its own terms lie far below the scales of other rows'), and every row of a
 // head with a non-finite value or s S' beyond fp16's range, is
 // computed by tree_row_exact. (A floor under the denominator instead of the bound sent one row in a
@@ -43,7 +43,7 @@ namespace favor {
 
 // Keys at most this far (log2) above the state's features leave X_r as it is.
 constexpr float kTreeTcRaise = 10.f;
-// s S' is scaled so that its first 64 features' largest magnitude is about 2^this.
+// A column of s S' is scaled so that its first 64 features' largest magnitude is about 2^this.
 constexpr float kTreeTcState = 6.f;
 
 template <int D_, bool STACK_>
@@ -61,7 +61,7 @@ struct TreeTc {
     static constexpr bool OVER = STACK_ && D == 64;          // the second low block takes W's first half
     static constexpr uint32_t OFF_W = KQ, OFF_XH = OFF_W + WB, OFF_XL = OFF_XH + NSB * XB,
                               OFF_F = OFF_XL + (OVER ? 1 : NSB) * XB;
-    static constexpr uint32_t OFF_BAR = OFF_F + 4 * (3 * 256 + 8 * 128 + 8 * 128 + 128 + 32 + 6 * 128), BYTES = OFF_BAR + 128 + 1024;
+    static constexpr uint32_t OFF_BAR = OFF_F + 4 * (3 * 256 + 8 * 128 + 8 * 128 + 128 + D + 16 + 6 * 128), BYTES = OFF_BAR + 128 + 1024;
     // TMEM columns: logits of a half (keys and queries), accumulators of A and Y, of the values' sum
     static constexpr uint32_t T_K = 0, T_Q = STACK_ ? 0 : 128, T_H = STACK_ ? 128 : 256, T_A = T_H, T_Y = T_A + MR,
                               T_O = (STACK_ && D == 128) ? 320 : T_A;
@@ -93,9 +93,9 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
     float *sDen = sMx, *sErr = sMx + 4 * 128;             // then [column group][128] parts of denominators and their errors
     float *sSum = sMx + 8 * 128;                          // [keys, queries][4][128] sums of a and b
     float *sGe = sSum + 8 * 128;                          // 2^(G_j - 30)
-    float *sRed = sGe + 128;                              // [16] warp maxima
-    int *sFlag = (int *)(sRed + 16);
-    int *sPar = (int *)(sRed + 32), *sPtr = sPar + 128;
+    float *sUp = sGe + 128;                               // [D] what the columns of s S' are multiplied by
+    int *sFlag = (int *)(sUp + D);
+    int *sPar = sFlag + 16, *sPtr = sPar + 128;
     uint32_t *sAnc = (uint32_t *)(sPtr + 128);            // [128][MR / 32] rows of J
     uint64_t *bars = (uint64_t *)(smem + C::OFF_BAR);
     uint64_t *kq_full = bars, *w_full = bars + 1, *v_full = bars + 2, *mma_done = bars + 3, *s_full = bars + 4;
@@ -180,7 +180,6 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
     const bool is_key = !STACK || (warp & 3) < 2, is_query = !STACK || (warp & 3) >= 2;
     const uint32_t tL = tmem + (((uint32_t)(warp & 3) * 32u) << 16);
     float eN = 0.f;     // -|k|^2/2 of this thread's key, log2 units
-    float shift = 0.f;  // s S' enters as 2^(kTreeTcState - shift) of itself
     bool v_asked = false;
     auto load_values = [&]() {
         if (warp == 0 && elect_one()) {
@@ -232,12 +231,13 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
             sFac[tid] = s;
         }
         const bool any_empty = __syncthreads_or(tid < m && !some), has_state = __syncthreads_or(tid < m && some);
-        // the size of s S', from its first 64 features
+        // the columns' sizes in s S', from its first 64 features: a lane a column and 16 features. (A column that
+        // is 0 there gets a scale that takes what later features may hold out of range, unless it is 0 in effect.)
         if (!wait(&s_full[0], 0)) break;
         {
-            float mx = 0.f;
             for (int rg = warp; rg < D / 8; rg += C::THREADS / 32) {
                 const int q = lane >> 3;
+                float mx = 0.f;
                 const uint8_t *src = (q < 2 ? sXH : sXL) + MR * 128 + rg * 1024;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -251,21 +251,16 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
                             if (y[k] < INFINITY) mx = fmaxf(mx, y[k]);
                     }
                 }
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                const int e = mx > 0.f ? min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 110) : -100;
+                if (lane < 8) sUp[8 * rg + lane] = __uint_as_float((uint32_t)(127 + (int)kTreeTcState - e) << 23);
             }
-            mx = warp_max(mx);
-            if (lane == 0) sRed[warp] = mx;
         }
         if (!wait(mma_done, nm++ & 1)) break;
         tc_fence_after();
         if (C::OVER && nch > 1) load_state();
         if (nh == 1) load_values();
-        {
-            float mx = sRed[0];
-#pragma unroll
-            for (int w = 1; w < min(D / 8, C::THREADS / 32); ++w) mx = fmaxf(mx, sRed[w]);
-            // its exponent (within 110, so that the scale of s_r S' stays a normal number)
-            shift = mx > 0.f ? (float)min(max((int)(__float_as_uint(mx) >> 23) - 127, -110), 110) : 0.f;
-        }
 
         // row maxima of P + sgn X over this thread's columns of a half
         auto row_max = [&](uint32_t col, int h, float sgn) {
@@ -357,7 +352,6 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
 
         float den_s[2] = {0.f, 0.f}, sum_a[2] = {0.f, 0.f}, sum_q[2] = {0.f, 0.f};  // 2^15 y_i, sum_r a_jr and b_ir, of this thread's features
         float(&sum_b)[2] = STACK ? sum_a : sum_q;  // (a thread of a stacked tile has a key or a query)
-        const float up = exp2f(kTreeTcState - shift);
         // 16 features from TMEM: 2^(15 + P + sgn X - max) as hi + lo
         auto split = [&](uint32_t col, int f, float sgn, float c, uint32_t(&hi)[8], uint32_t(&lo)[8], float(&sum)[2], bool state) {
             float v[16];
@@ -421,6 +415,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
             for (int t = warp; t < (c1 - c0) * (D / 8); t += C::THREADS / 32) {
                 const int c = c0 + t / (D / 8), rg = t % (D / 8), s = c % NSB, q = lane >> 3, r = 64 * c + 16 * q;
                 uint8_t *xh = sXH + s * C::XB + MR * 128 + rg * 1024, *xl = (s == 0 ? sXL : sXL1) + MR * 128 + rg * 1024;
+                const float up = sUp[8 * rg + (lane & 7)];
                 uint32_t hi[8], lo[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -593,7 +588,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
             // (measured against 64 bits at m = 32, 128, 256: 1.9e-7, 3.3e-7, 7.3e-7 low in all), while y_i is
             // summed with rounding; what is expected to be missing is added back.
             const float lost = 1.8e-8f * (float)(min(m, 64 * NSB) / 16 + 3 * max(m - 64 * NSB, 0) / 16);
-            const float fy = ex2_approx(shift - kTreeTcState - 15.f) * (1.f + lost);
+            const float fy = 0x1p-15f * (1.f + lost);
             constexpr int CT = D / NCG;  // columns a thread takes
 #pragma unroll
             for (int q = 0; q < CT; q += 16) {
@@ -607,7 +602,10 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
                 for (int e = 0; e < 16; e += 4) {
                     float x[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) x[k] = (has_state ? fmaf(fy, y[e + k], o[e + k]) : o[e + k]) * inv;
+                    for (int k = 0; k < 4; ++k) {  // (1 / up: powers of two)
+                        const float down = __uint_as_float((254u << 23) - __float_as_uint(sUp[c0 + e + k]));
+                        x[k] = (has_state ? fmaf(fy * down, y[e + k], o[e + k]) : o[e + k]) * inv;
+                    }
                     *(float4 *)(sOut + row * D + ((((c0 + e) >> 2) ^ (row & 7)) << 2)) = make_float4(x[0], x[1], x[2], x[3]);
                 }
             }

@@ -236,6 +236,44 @@ def test_tree_over_features_of_very_different_sums(cuda_device, dtype, factor):
         assert rel_max_err(out[b, h], ref) <= TOL
 
 
+def column_scales(d, lowest, device):
+    """Powers of two from 1 down to 2^lowest, one per value column, neighbours far apart (exact in any type)."""
+    e = torch.round(torch.linspace(0, lowest, d))[torch.randperm(d, generator=torch.Generator().manual_seed(d))]
+    return torch.exp2(e).to(device)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lowest", [-20, -60])
+@pytest.mark.parametrize("B,H,T,d,m", [(1, 2, 40, 64, 256), (1, 2, 100, 128, 128), (25, 16, 64, 64, 256), (25, 16, 30, 128, 96),
+                                       (25, 16, 100, 64, 128), (1, 2, 12, 64, 256), (1, 2, 4, 128, 64)])
+def test_tree_value_columns_of_very_different_size(cuda_device, dtype, lowest, B, H, T, d, m):
+    """Each output column to the tolerance of its own largest entry (some heads checked)."""
+    x = Problem(B, H, T, d, m, dtype, cuda_device, prior=0, seed=T + d)
+    scales = column_scales(d, lowest, cuda_device).to(x.v.dtype)
+    x.v *= scales
+    state = api.decode_extend(x.tokens(50, d ** -0.25), x.tokens(50, 1.0) * scales, x.W, x.state)
+    parents = random_parents(B, T, seed=T)
+    out = api.decode_tree(x.q, x.k, x.v, x.W, state, i32(parents, cuda_device)).double().cpu().numpy()
+    status_ok()
+    for (b, h), ref in tree_from_state(x, state, parents, [T] * B, [(0, 0), (0, 1), (B - 1, H - 1)]).items():
+        assert (np.abs(out[b, h] - ref).max(0) <= TOL * np.abs(ref).max(0)).all()
+
+
+@pytest.mark.parametrize("factor", [1.0, 2.0**-30, 2.0**30])
+def test_tree_value_columns_that_only_later_features_hold(cuda_device, factor):
+    """Columns of S' that are 0 in the first 64 features, whose size the column's scale comes from."""
+    x = Problem(1, 2, 40, 64, 192, "bf16", cuda_device, seed=51)
+    state = x.state.clone()
+    state.view(2, 66, 192)[:, 3:9, :64] = 0
+    state.view(2, 66, 192)[:, 3:9] *= factor
+    x.v[:, :, :, 3:9] *= factor
+    parents = random_parents(1, 40, seed=51)
+    out = api.decode_tree(x.q, x.k, x.v, x.W, state, i32(parents, cuda_device)).double().cpu().numpy()
+    status_ok()
+    for (b, h), ref in tree_from_state(x, state, parents, [40], [(0, 0), (0, 1)]).items():
+        assert (np.abs(out[b, h] - ref).max(0) <= TOL * np.abs(ref).max(0)).all()
+
+
 def test_tree_bad_parents_and_counts_are_recorded(cuda_device):
     T = 20
     x = Problem(2, 2, T, 64, 128, "bf16", cuda_device, seed=8)
@@ -416,12 +454,6 @@ def test_extend_values_that_grow_along_the_sequence(cuda_device, dtype):
     state = api.decode_extend(x.k, x.v, x.W, x.state)
     status_ok()
     check_state(x, state, [None])
-
-
-def column_scales(d, lowest, device):
-    """Powers of two from 1 down to 2^lowest, one per value column, neighbours far apart (exact in any type)."""
-    e = torch.round(torch.linspace(0, lowest, d))[torch.randperm(d, generator=torch.Generator().manual_seed(d))]
-    return torch.exp2(e).to(device)
 
 
 @pytest.mark.parametrize("dtype,indexed", [("bf16", False), ("bf16", True), ("f32", False)])
