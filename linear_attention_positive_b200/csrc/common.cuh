@@ -306,7 +306,7 @@ __device__ __forceinline__ void mma_ss_x4_w(uint32_t d, uint64_t a, uint64_t b, 
         : "memory");
 }
 __device__ __forceinline__ void mma_ts_x4_w(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc,
-                                            uint32_t b_step) {
+                                            uint32_t b_step, uint32_t a_step = 8) {
     const uint64_t b1 = b + b_step, b2 = b1 + b_step, b3 = b2 + b_step;
     asm volatile(
         "{\n\t.reg .pred p, t, e;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 t, %6, %6;\n\t" FAVOR_ELECT
@@ -314,8 +314,8 @@ __device__ __forceinline__ void mma_ts_x4_w(uint32_t d, uint32_t a_tmem, uint64_
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%7], %3, %5, t;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%8], %4, %5, t;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%9], %10, %5, t;\n\t}" ::"r"(d),
-        "r"(a_tmem), "l"(b), "l"(b1), "l"(b2), "r"(idesc), "r"(acc), "r"(a_tmem + 8), "r"(a_tmem + 16),
-        "r"(a_tmem + 24), "l"(b3)
+        "r"(a_tmem), "l"(b), "l"(b1), "l"(b2), "r"(idesc), "r"(acc), "r"(a_tmem + a_step), "r"(a_tmem + 2 * a_step),
+        "r"(a_tmem + 3 * a_step), "l"(b3)
         : "memory");
 }
 __device__ __forceinline__ void mma_commit_w(uint64_t *bar) {

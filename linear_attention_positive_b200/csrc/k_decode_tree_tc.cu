@@ -65,8 +65,10 @@ struct TreeTc {
     // TMEM columns: logits of a half (keys and queries), accumulators of A and Y, of the values' sum
     static constexpr uint32_t T_K = 0, T_Q = STACK_ ? 0 : 128, T_H = STACK_ ? 128 : 256, T_A = T_H, T_Y = T_A + MR,
                               T_O = (STACK_ && D == 128) ? 320 : T_A;
+    static constexpr uint32_t OFF_Y = OFF_W + (OVER ? NB * BLK : 0);  // the first half's Y, fp32 [MR][D], in W's place
     static constexpr uint32_t COLS = (STACK_ && D == 64) ? 256 : 512;
-    static_assert(MR * D * 4 <= WB && (!OVER || XB <= NB * BLK), "output rows and the low block fit in W's place");
+    static_assert(MR * D * 4 <= WB && (!OVER || (XB <= NB * BLK && MR * D * 4 <= NB * BLK)),
+                  "output rows, the low block and the first half's Y fit in W's place");
 };
 
 // fp32 order as signed integers (for the integer warp maximum) and back.
@@ -75,6 +77,9 @@ __device__ __forceinline__ int order_bits(float x) {
     return i ^ ((i >> 31) & 0x7fffffff);
 }
 __device__ __forceinline__ float from_order_bits(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+
+// The 11 leading bits of x, rounded to nearest.
+__device__ __forceinline__ float hi_round(float x) { return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xFFFFE000u); }
 
 template <int D, bool STACK>
 __global__ void __launch_bounds__(TreeTc<D, STACK>::THREADS, (STACK && D == 64) ? 2 : 1)
@@ -179,6 +184,8 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
     const int row = STACK ? (warp & 1) * 32 + lane : (warp & 3) * 32 + lane, cg = warp >> 2;
     const bool is_key = !STACK || (warp & 3) < 2, is_query = !STACK || (warp & 3) >= 2;
     const uint32_t tL = tmem + (((uint32_t)(warp & 3) * 32u) << 16);
+    float *sY = (float *)(smem + C::OFF_Y);
+    auto row_chunk = [&](int c) { return row * D + (((c >> 2) ^ (row & 7)) << 2); };  // 16-byte chunks XOR-swizzled by row
     float eN = 0.f;     // -|k|^2/2 of this thread's key, log2 units
     bool v_asked = false;
     auto load_values = [&]() {
@@ -371,7 +378,8 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
                     y0 = ex2_approx(y0);
                     y1 = ex2_approx(y1);
                     ffma2(y0, y1, 0x1p15f, 0x1p15f, 0.f, 0.f, y0, y1);
-                    const float h0 = tf32_trunc(y0), h1 = tf32_trunc(y1);
+                    // (the keys' hi is rounded, the queries' truncated: lo lo, which is left out, then has no sign)
+                    const float h0 = state ? tf32_trunc(y0) : hi_round(y0), h1 = state ? tf32_trunc(y1) : hi_round(y1);
                     ffma2(y0, y1, 1.f, 1.f, sum[0], sum[1], sum[0], sum[1]);
                     if (state) ffma2(y0, y1, s[k], s[k + 1], den_s[0], den_s[1], den_s[0], den_s[1]);
                     ffma2(h0, h1, -1.f, -1.f, y0, y1, l0, l1);
@@ -426,7 +434,7 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
                     float yh[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        yh[k] = tf32_trunc(y[k]);
+                        yh[k] = hi_round(y[k]);
                         bad = bad || !(fabsf(yh[k]) < 65504.f);
                     }
                     hi[2 * i] = pack_f16x2(yh[0], yh[1]);
@@ -452,16 +460,27 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
                 // K-steps of 16 features: hi lo and lo hi of all, then hi hi. (Each addition truncates the
                 // accumulator; the first two thirds of a first half's then truncate a small one.)
                 constexpr uint32_t idesc_x = make_idesc(128, MR + D, kFmtF16, 0, 0);
+                constexpr uint32_t idesc_a = make_idesc(128, MR, kFmtF16, 0, 0), idesc_y = make_idesc(128, D, kFmtF16, 0, 0);
                 const uint64_t dXH = make_sdesc(smem_u32(sXH), 16, 1024), dXL = make_sdesc(smem_u32(sXL), 16, 1024);
                 const uint64_t dXL1 = make_sdesc(smem_u32(sXL1), 16, 1024);
-                const int k0 = 4 * c0, k1 = min(m, 64 * c1) / 16;
 #pragma unroll 1
                 for (int i = 0; i < 3; ++i)
 #pragma unroll 1
-                    for (int k = k0; k < k1; ++k) {
-                        const int s = (k >> 2) % NSB;
-                        const uint64_t x = (i != 0 ? dXH : s == 0 ? dXL : dXL1) + (i != 0 ? s * (C::XB / 16) : 0) + 2 * (k & 3);
-                        mma_f16_ts_w(tmem + C::T_A, tmem + C::T_Q + 16 * (k & 7) + (i == 1 ? 8 : 0), x, idesc_x, k + i > 0);
+                    for (int c = c0; c < c1; ++c) {  // 64 features: four steps, or two at the end of m
+                        const int s = c % NSB;
+                        const uint64_t x = i != 0 ? dXH + s * (C::XB / 16) : s == 0 ? dXL : dXL1;
+                        const uint32_t b = tmem + C::T_Q + 64 * (c & 1) + (i == 1 ? 8 : 0);
+                        if (c == 2 && i == 0) {  // the second half's Y starts anew
+                            mma_f16_ts_w(tmem + C::T_A, b, x, idesc_a, 1u);
+                            mma_f16_ts_w(tmem + C::T_Y, b, x + MR * 128 / 16, idesc_y, 0u);
+                            for (int k = 1; k < (m - 128 < 64 ? 2 : 4); ++k)
+                                mma_f16_ts_w(tmem + C::T_A, b + 16 * k, x + 2 * k, idesc_x, 1u);
+                        } else if (64 * c + 64 <= m) {
+                            mma_ts_x4_w(tmem + C::T_A, b, x, idesc_x, c + i > 0, 2, 16);
+                        } else {
+                            mma_f16_ts_w(tmem + C::T_A, b, x, idesc_x, c + i > 0);
+                            mma_f16_ts_w(tmem + C::T_A, b + 16, x + 2, idesc_x, 1u);
+                        }
                     }
                 mma_commit_w(mma_done);
             }
@@ -480,6 +499,18 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
                 if (!wait(mma_done, nm++ & 1)) break;
                 tc_fence_after();
                 load_values();
+                // Y of the first half moves out (T_Y starts anew): each addition truncates the accumulator by up to
+                // 2^-23 of it, while y_i is summed with rounding. Equal values then come out 6e-7 low at m = 256, and
+                // 2e-6 low where one accumulator holds both halves (0.6 us of 43 for 256 heads of 60 nodes at d = 128).
+                if (is_query) {
+#pragma unroll 1
+                    for (int c = cg * (D / NCG); c < (cg + 1) * (D / NCG); c += 16) {
+                        float y[16];
+                        tmem_ld16(tL + C::T_Y + c, y);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) *(float4 *)(sY + row_chunk(c + e)) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                    }
+                }
             }
         }
         if (!ok) break;
@@ -584,11 +615,6 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
         float *sOut = (float *)sW;
         if (is_query) {
             if (cg == 0) sPtr[row] = good && sFlag[0] == 0;
-            // Y's accumulator was truncated by each addition at its full size, 1.8e-8 of it a time on average
-            // (measured against 64 bits at m = 32, 128, 256: 1.9e-7, 3.3e-7, 7.3e-7 low in all), while y_i is
-            // summed with rounding; what is expected to be missing is added back.
-            const float lost = 1.8e-8f * (float)(min(m, 64 * NSB) / 16 + 3 * max(m - 64 * NSB, 0) / 16);
-            const float fy = 0x1p-15f * (1.f + lost);
             constexpr int CT = D / NCG;  // columns a thread takes
 #pragma unroll
             for (int q = 0; q < CT; q += 16) {
@@ -601,12 +627,16 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
                     float x[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {  // (1 / up: powers of two)
-                        const float down = __uint_as_float((254u << 23) - __float_as_uint(sUp[c0 + e + k]));
-                        x[k] = (has_state ? fmaf(fy * down, y[e + k], o[e + k]) : o[e + k]) * inv;
+                    if (nh == 2) {
+                        const float4 y1 = *(const float4 *)(sY + row_chunk(c0 + e));
+                        y[e] += y1.x, y[e + 1] += y1.y, y[e + 2] += y1.z, y[e + 3] += y1.w;
                     }
-                    *(float4 *)(sOut + row * D + ((((c0 + e) >> 2) ^ (row & 7)) << 2)) = make_float4(x[0], x[1], x[2], x[3]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {  // (2^-15 / up: powers of two)
+                        const float down = __uint_as_float((239u << 23) - __float_as_uint(sUp[c0 + e + k]));
+                        x[k] = (has_state ? fmaf(down, y[e + k], o[e + k]) : o[e + k]) * inv;
+                    }
+                    *(float4 *)(sOut + row_chunk(c0 + e)) = make_float4(x[0], x[1], x[2], x[3]);
                 }
             }
         }

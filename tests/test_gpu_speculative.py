@@ -274,6 +274,22 @@ def test_tree_value_columns_that_only_later_features_hold(cuda_device, factor):
         assert (np.abs(out[b, h] - ref).max(0) <= TOL * np.abs(ref).max(0)).all()
 
 
+@pytest.mark.parametrize("T,d,m", [(40, 64, 256), (64, 64, 160), (60, 128, 256), (100, 64, 256), (100, 128, 256), (40, 64, 64)])
+def test_tree_equal_values_come_out_as_they_are(cuda_device, T, d, m):
+    """Values of 1 everywhere give 1: numerator and denominator are the same sums. The tensor core's additions
+    truncate, each by less than 2^-23 of the accumulator. Per 128 features eight of them see a full one (above 64
+    nodes at d = 128, where 64 features are taken at a time, sixteen); the operands' parts add 2^-23 at most."""
+    x = Problem(8, 8, T, d, m, "bf16", cuda_device, prior=0, seed=m + T)
+    state = api.decode_extend(x.tokens(70, d ** -0.25), x.tokens(70, 1.0), x.W, x.state).view(64, d + 2, m)
+    state[:, :d] = state[:, d:d + 1]
+    x.v.fill_(1)
+    out = api.decode_tree(x.q, x.k, x.v, x.W, state.view(-1), i32(random_parents(8, T, seed=T), cuda_device))
+    status_ok()
+    steps = 16 if T > 64 and d == 128 else 8
+    assert abs(out.double().mean().item() - 1) <= (steps + 1) * 2.0**-23
+    assert (out - 1).abs().max().item() <= TOL
+
+
 def test_tree_bad_parents_and_counts_are_recorded(cuda_device):
     T = 20
     x = Problem(2, 2, T, 64, 128, "bf16", cuda_device, seed=8)
