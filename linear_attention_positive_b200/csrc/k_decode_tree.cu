@@ -13,7 +13,7 @@
 // What can still be lost is a row whose visible terms are all e^-87 or more below the features'
 // maxima E_r, which nodes it does not see may have set. Its denominator then comes out below
 // kTreeDenMin and the row is recomputed in log space from its own visible terms alone
-// (tree_row_exact); the same path takes nothing from nodes outside J(i), so NaN or infinities there
+// (tree_row_exact, tree_row_exact_bf16); the same path takes nothing from nodes outside J(i), so NaN or infinities there
 // never reach a row.
 
 #include "common.cuh"
@@ -69,37 +69,23 @@ __device__ __forceinline__ int tree_parent(const int *parents, int i) {
     return p;
 }
 
-// w_r . x from global memory (one thread; 16-byte loads).
+// w_r . x from global memory in fp32 (one thread; 16-byte loads).
 template <int D>
-__device__ float dot_global(const void *W, const void *x, int bf16, int r, size_t x0) {
+__device__ float dot_global(const void *W, const void *x, int r, size_t x0) {
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    if (bf16) {
-        const uint4 *w = (const uint4 *)((const uint16_t *)W + (size_t)r * D), *y = (const uint4 *)((const uint16_t *)x + x0);
+    const float4 *w = (const float4 *)((const float *)W + (size_t)r * D), *y = (const float4 *)((const float *)x + x0);
 #pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-            const uint4 a = __ldg(w + i), c = __ldg(y + i);
-            const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                acc[j] = fmaf(__uint_as_float(u[j] << 16), __uint_as_float(v[j] << 16), acc[j]);
-                acc[j] = fmaf(__uint_as_float(u[j] & 0xFFFF0000u), __uint_as_float(v[j] & 0xFFFF0000u), acc[j]);
-            }
-        }
-    } else {
-        const float4 *w = (const float4 *)((const float *)W + (size_t)r * D), *y = (const float4 *)((const float *)x + x0);
-#pragma unroll 4
-        for (int i = 0; i < D / 4; ++i) {
-            const float4 a = __ldg(w + i), c = __ldg(y + i);
-            acc[0] = fmaf(a.x, c.x, acc[0]);
-            acc[1] = fmaf(a.y, c.y, acc[1]);
-            acc[2] = fmaf(a.z, c.z, acc[2]);
-            acc[3] = fmaf(a.w, c.w, acc[3]);
-        }
+    for (int i = 0; i < D / 4; ++i) {
+        const float4 a = __ldg(w + i), c = __ldg(y + i);
+        acc[0] = fmaf(a.x, c.x, acc[0]);
+        acc[1] = fmaf(a.y, c.y, acc[1]);
+        acc[2] = fmaf(a.z, c.z, acc[2]);
+        acc[3] = fmaf(a.w, c.w, acc[3]);
     }
     return (acc[0] + acc[1]) + (acc[2] + acc[3]);
 }
 
-// One output row in log space over its own visible terms (one warp; lanes over features, then over
+// One output row in log space over its own visible terms, fp32 (one warp; lanes over features, then over
 // value columns): F = the row's largest exponent, weight_j = sum_r e^(w_r.q + u_r(k_j) - F). `par`
 // holds the checked parents. Rare, so its projections are simply recomputed.
 template <int D>
@@ -111,13 +97,13 @@ __device__ __noinline__ void tree_row_exact(const TreeParams &p, int bh, int i, 
     float uq[8], F = -INFINITY;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        uq[k] = k < nk ? dot_global<D>(p.W, p.q, p.bf16, lane + 32 * k, row0 + (size_t)i * D) : -INFINITY;
+        uq[k] = k < nk ? dot_global<D>(p.W, p.q, lane + 32 * k, row0 + (size_t)i * D) : -INFINITY;
         if (k < nk && z[lane + 32 * k] != 0.f) F = fmaxf(F, uq[k] + Dl[lane + 32 * k]);
     }
     auto half_norm = [&](int j) {
         float s = 0.f;
         for (int c = lane; c < D; c += 32) {
-            const float x = ld_elem(p.k, p.bf16, row0 + (size_t)j * D + c);
+            const float x = ld_elem(p.k, 0, row0 + (size_t)j * D + c);
             s = fmaf(x, x, s);
         }
         return 0.5f * warp_sum(s);
@@ -127,7 +113,7 @@ __device__ __noinline__ void tree_row_exact(const TreeParams &p, int bh, int i, 
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             if (k < nk)
-                F = fmaxf(F, uq[k] + dot_global<D>(p.W, p.k, p.bf16, lane + 32 * k, row0 + (size_t)j * D) - h);
+                F = fmaxf(F, uq[k] + dot_global<D>(p.W, p.k, lane + 32 * k, row0 + (size_t)j * D) - h);
     }
     F = warp_max(F);
     float num[D / 32], den = 0.f;
@@ -156,15 +142,147 @@ __device__ __noinline__ void tree_row_exact(const TreeParams &p, int bh, int i, 
         float w = 0.f;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            if (k < nk) w += expf(uq[k] + dot_global<D>(p.W, p.k, p.bf16, lane + 32 * k, row0 + (size_t)j * D) - h);
+            if (k < nk) w += expf(uq[k] + dot_global<D>(p.W, p.k, lane + 32 * k, row0 + (size_t)j * D) - h);
         w = warp_sum(w);
         den += w;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-            const float x = ld_elem(p.v, p.bf16, row0 + (size_t)j * D + lane + 32 * c);
+            const float x = ld_elem(p.v, 0, row0 + (size_t)j * D + lane + 32 * c);
             num[c] = w == 0.f ? num[c] : fmaf(w, x, num[c]);
         }
     }
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) p.out[row0 + (size_t)i * D + lane + 32 * c] = num[c] / den;
+}
+
+// The same for bf16 by warp MMAs (exact products), q and 7 visible nodes at a time, 64 features after
+// another with a running F, so that W is read once for 7 nodes and little is held: a lane has features
+// 16 f + 8 h + g of rows 2 t and 2 t + 1 (row 0: q), g = lane / 4, t = lane % 4. At m = 256 a row of some 25
+// nodes adds 40 us to a call at d = 64 and 80 at d = 128 (one node at a time, each lane reading its features'
+// rows of W, twice: 170 and 560).
+template <int D>
+__device__ __noinline__ void tree_row_exact_bf16(const TreeParams &p, int bh, int i, const int *par) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, m = p.m;
+    const size_t row0 = (size_t)bh * p.T * D;
+    const float *S = p.state + (size_t)bh * ((size_t)D * m + 2 * m), *z = S + (size_t)D * m, *Dl = z + m;
+    auto over_g = [](float x) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        return x;
+    };
+    float num[D / 32], den = 0.f, dz = 0.f, F = -INFINITY;  // dz: the state's part of the denominator, this lane's features
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) num[k] = 0.f;
+    for (int j = i; j >= 0;) {
+        const bool first = j == i;  // the state is taken along
+        int mine = -1;
+#pragma unroll
+        for (int k = 1; k < 8; ++k) {
+            if (k == g) mine = j;
+            j = j >= 0 ? par[j] : -1;
+        }
+        const uint16_t *x = (const uint16_t *)(g == 0 ? p.q : p.k) + row0 + (size_t)(g == 0 ? i : max(mine, 0)) * D + 8 * t;
+        uint4 xb[D / 32];
+        float sq = 0.f, h[2], w[2] = {0.f, 0.f};
+        bool use[2];
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+            xb[k] = g == 0 || mine >= 0 ? __ldg((const uint4 *)(x + 32 * k)) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t u[4] = {xb[k].x, xb[k].y, xb[k].z, xb[k].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float lo = __uint_as_float(u[q] << 16), hi = __uint_as_float(u[q] & 0xFFFF0000u);
+                sq = fmaf(lo, lo, sq);
+                sq = fmaf(hi, hi, sq);
+            }
+        }
+        sq += __shfl_xor_sync(0xffffffffu, sq, 1);
+        sq += __shfl_xor_sync(0xffffffffu, sq, 2);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            h[q] = 0.5f * __shfl_sync(0xffffffffu, sq, 4 * (2 * t + q));
+            use[q] = __shfl_sync(0xffffffffu, mine, 4 * (2 * t + q)) >= 0;
+        }
+#pragma unroll 1
+        for (int f0 = 0; f0 < m; f0 += 64) {
+            float u[4][4], e[8], top = -INFINITY;
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                const int r = f0 + 16 * f + g;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) u[f][q] = 0.f;
+                if (f0 + 16 * f < m) {
+                    const uint16_t *W = (const uint16_t *)p.W + (size_t)r * D + 8 * t;
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k) {
+                        const uint4 a = __ldg((const uint4 *)(W + 32 * k)), b = __ldg((const uint4 *)(W + 8 * D + 32 * k));
+                        mma_bf16_16x8x16(u[f], a.x, b.x, a.y, b.y, xb[k].x, xb[k].y);
+                        mma_bf16_16x8x16(u[f], a.z, b.z, a.w, b.w, xb[k].z, xb[k].w);
+                    }
+                }
+                const bool in = f0 + 16 * f < m;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float uq = __shfl_sync(0xffffffffu, u[f][2 * q], lane & 28);
+                    e[2 * f + q] = first && in && z[r + 8 * q] != 0.f ? uq + Dl[r + 8 * q] : -INFINITY;
+                    u[f][2 * q] = in && use[0] ? uq + u[f][2 * q] - h[0] : -INFINITY;
+                    u[f][2 * q + 1] = in && use[1] ? uq + u[f][2 * q + 1] - h[1] : -INFINITY;
+                    top = fmax3(top, e[2 * f + q], fmaxf(u[f][2 * q], u[f][2 * q + 1]));
+                }
+            }
+            top = fmaxf(F, warp_max(top));
+            if (top > F) {
+                const float keep = expf(F - top);  // (0 at first)
+                F = top;
+                den *= keep;
+                dz *= keep;
+                w[0] *= keep;
+                w[1] *= keep;
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) num[k] *= keep;
+            }
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) w[q & 1] += use[q & 1] && f0 + 16 * f < m ? expf(u[f][q] - F) : 0.f;
+            if (first) {
+#pragma unroll
+                for (int f = 0; f < 8; ++f) {
+                    e[f] = e[f] == -INFINITY ? 0.f : expf(e[f] - F);
+                    if (e[f] != 0.f) dz = fmaf(e[f], z[f0 + 8 * f + g], dz);
+                }
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k)
+#pragma unroll 4
+                    for (int c = 0; c < 8; ++c) {  // columns 32 k + 4 c + t
+                        const float *at = S + (size_t)(32 * k + 4 * c + t) * m + f0 + g;
+                        float y = 0.f;
+#pragma unroll
+                        for (int f = 0; f < 8; ++f)
+                            if (e[f] != 0.f) y = fmaf(e[f], at[8 * f], y);
+                        y = over_g(y);
+                        if (c == g) num[k] += y;
+                    }
+            }
+        }
+        w[0] = over_g(w[0]);
+        w[1] = over_g(w[1]);
+        float v[7][D / 32];
+#pragma unroll
+        for (int k = 1; k < 8; ++k) {
+            const int at = __shfl_sync(0xffffffffu, mine, 4 * k);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) v[k - 1][c] = at >= 0 ? ld_elem(p.v, 1, row0 + (size_t)at * D + lane + 32 * c) : 0.f;
+        }
+#pragma unroll
+        for (int k = 1; k < 8; ++k) {
+            const float y = __shfl_sync(0xffffffffu, w[k & 1], k >> 1);  // 0 where there is no node
+            den += y;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) num[c] = y == 0.f ? num[c] : fmaf(y, v[k - 1][c], num[c]);
+        }
+    }
+    den += over_g(dz);
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) p.out[row0 + (size_t)i * D + lane + 32 * c] = num[c] / den;
 }
@@ -434,7 +552,12 @@ __global__ void __launch_bounds__(256, 1) k_decode_tree_few(TreeParams p) {
     }
     if (c0 == 0)
         for (int t = warp; t < n; t += nw)
-            if (!(sC[2 * t + 1] >= kTreeDenMin)) tree_row_exact<D>(p, bh, t, sPar);
+            if (!(sC[2 * t + 1] >= kTreeDenMin)) {
+                if (p.bf16)
+                    tree_row_exact_bf16<D>(p, bh, t, sPar);
+                else
+                    tree_row_exact<D>(p, bh, t, sPar);
+            }
 }
 
 template <int D, int TT>
@@ -734,7 +857,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_decode_tree_rows(TreeParams
     }
     if (c0 == 0)
         for (int i = warp; i < rows; i += nw)
-            if (!(sC[4 * i + 2] >= kTreeDenMin)) tree_row_exact<D>(p, bh, i0 + i, sPar);
+            if (!(sC[4 * i + 2] >= kTreeDenMin)) {
+                if constexpr (BF16)
+                    tree_row_exact_bf16<D>(p, bh, i0 + i, sPar);
+                else
+                    tree_row_exact<D>(p, bh, i0 + i, sPar);
+            }
 }
 
 template <int D, bool BF16>

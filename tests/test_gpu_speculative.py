@@ -274,6 +274,27 @@ def test_tree_value_columns_that_only_later_features_hold(cuda_device, factor):
         assert (np.abs(out[b, h] - ref).max(0) <= TOL * np.abs(ref).max(0)).all()
 
 
+@pytest.mark.parametrize("T,d,m,prior,scale", [(64, 64, 32, 2, 2.0), (64, 64, 32, 0, 3.0), (60, 128, 32, 1, 1.0), (100, 64, 32, 2, 2.0)])
+def test_tree_rows_whose_terms_lie_below_the_scales_of_others(cuda_device, T, d, m, prior, scale):
+    """Many roots over a short context, all heads: rows whose own terms are small next to what sets the features'
+    scales. |w| |x| stays within the 80 of the bound above (|w| ~ 11, |x| ~ 7), so its tolerance applies."""
+    B, H = 16, 8
+    x = Problem(B, H, T, d, m, "bf16", cuda_device, prior=0, seed=m + T)
+    x.q *= min(scale, 2.0)
+    x.k *= scale
+    state = x.state
+    if prior:
+        state = api.decode_extend(x.tokens(prior, scale * d ** -0.25), x.tokens(prior, 1.0), x.W, state)
+    parents = random_parents(B, T, seed=T, reach=8)
+    parents[:, ::3] = -1
+    out = api.decode_tree(x.q, x.k, x.v, x.W, state, i32(parents, cuda_device)).double().cpu().numpy()
+    status_ok()
+    heads = [(b, h) for b in range(B) for h in range(H)]
+    ref = tree_from_state(x, state, parents, [T] * B, heads)
+    ref = np.stack([ref[at] for at in heads]).reshape(out.shape)
+    assert rel_max_err(out, ref) <= TOL
+
+
 @pytest.mark.parametrize("T,d,m", [(40, 64, 256), (64, 64, 160), (60, 128, 256), (100, 64, 256), (100, 128, 256), (40, 64, 64)])
 def test_tree_equal_values_come_out_as_they_are(cuda_device, T, d, m):
     """Values of 1 everywhere give 1: numerator and denominator are the same sums. The tensor core's additions
