@@ -236,6 +236,26 @@ def test_tree_over_features_of_very_different_sums(cuda_device, dtype, factor):
         assert rel_max_err(out[b, h], ref) <= TOL
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,m", [(1, 64, 256), (2, 128, 96), (3, 64, 32), (4, 128, 256), (4, 64, 256)])
+def test_tree_of_few_nodes_of_a_full_batch(cuda_device, dtype, T, d, m):
+    """Up to four nodes in more heads than fit the device at once, counts cut differently (some heads checked)."""
+    B, H = 25, 16
+    x = Problem(B, H, T, d, m, dtype, cuda_device, prior=0, seed=T + d)
+    state = api.decode_extend(x.tokens(70, d ** -0.25), x.tokens(70, 1.0), x.W, x.state)
+    parents = random_parents(B, T, seed=T, reach=2)
+    counts = np.random.default_rng(T).integers(0, T + 1, B)
+    counts[:3] = T, 0, 1
+    out = torch.full((B, H, T, d), 7.0, device=cuda_device)
+    api.decode_tree(x.q, x.k, x.v, x.W, state, i32(parents, cuda_device), n_nodes=i32(counts, cuda_device), out=out)
+    status_ok()
+    got = out.double().cpu().numpy()
+    for (b, h), ref in tree_from_state(x, state, parents, counts, [(0, 0), (0, 15), (2, 5), (9, 9), (24, 15)]).items():
+        assert rel_max_err(got[b, h, : counts[b]], ref) <= TOL if counts[b] else True
+    for b in range(B):
+        assert (got[b, :, counts[b]:] == 7.0).all()
+
+
 def column_scales(d, lowest, device):
     """Powers of two from 1 down to 2^lowest, one per value column, neighbours far apart (exact in any type)."""
     e = torch.round(torch.linspace(0, lowest, d))[torch.randperm(d, generator=torch.Generator().manual_seed(d))]
@@ -469,6 +489,24 @@ def test_extend_keys_far_above_and_below_earlier_ones(cuda_device, dtype, L):
         S, z = x.gpu_state(state)
         assert (np.abs(z[0, h] - zr) <= 7 * TOL * zr).all()
         assert (np.abs(S[0, h] - Sr) <= 7 * TOL * np.abs(Sr).max(1, keepdims=True)).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("at", [[500], [63, 64, 700], [200, 330, 460, 590, 720, 1000]])
+def test_extend_keys_far_above_within_a_run_of_many_tiles(cuda_device, d, at):
+    """Each head takes its tokens in one or two runs of many tiles; keys along a row of W raise D_r in the middle
+    (some heads checked, per feature; u reaches |w| |x| ~ 16 * 16, 4 times the bound above)."""
+    B, H, L, m = 20, 8, 1100, 256
+    x = Problem(B, H, L, d, m, "bf16", cuda_device, prior=0, seed=d)
+    for n, j in enumerate(at):
+        x.k[:, :, j] = (0.9 * x.W[17 * n].float()).to(x.k.dtype)
+    state = api.decode_extend(x.k, x.v, x.W, x.state)
+    status_ok()
+    S, z = x.gpu_state(state)
+    for b, h in [(0, 0), (7, 3), (13, 7), (19, 7)]:
+        Sr, zr = speculative.decode_extend(np.zeros((m, d)), np.zeros(m), x.head(x.k, b, h), x.head(x.v, b, h), x.W64)
+        assert (np.abs(z[b, h] - zr) <= 4 * TOL * zr).all()
+        assert (np.abs(S[b, h] - Sr) <= 4 * TOL * np.abs(Sr).max(1, keepdims=True)).all()
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

@@ -142,3 +142,44 @@ def test_decode_extend_refuses_token_counts_whose_runs_would_pass_32_bits(favor_
             assert f(few, P, P, P, P, n, P, P, P, 1 << 40, NULL) == UNSUPPORTED
         assert size(many, 0) == 0
         assert f(many, P, P, P, NULL, 0, P, P, P, 1 << 40, NULL) == UNSUPPORTED
+
+
+def test_calls_run_with_the_tensors_device_current(monkeypatch):
+    """On the tensors' device and its current stream, or the given one (stand-ins for CUDA)."""
+    current, seen = [0], []
+
+    class Device:
+        def __init__(self, device):
+            self.index = device.index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *_):
+            current[0] = self.before
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+
+    def entry(*args):
+        seen.append((current[0],) + args)
+        return api.FAVOR_OK
+
+    class Stream:
+        cuda_stream = 77
+
+    for index in (0, 1):
+        api._launch("call", entry, torch.device("cuda", index), None, "a")
+        api._launch("call", entry, torch.device("cuda", index), Stream, "b")
+    assert seen == [(0, "a", 100), (0, "b", 77), (1, "a", 101), (1, "b", 77)]
+    assert current == [0]
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    with pytest.raises(api.FavorError) as e:
+        api._empty((4,), torch.float32, torch.device("cuda", 0), Stream)
+    assert e.value.status == INVALID
