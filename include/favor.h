@@ -293,7 +293,8 @@ FAVOR_API size_t favor_decode_extend_workspace_size(const favor_shape *shape, in
  *   stream       : cudaStream_t as void*
  * k, v, W, state 16-byte aligned, index and counts 4-byte. fp32 precision for either dtype, in each value
  * column relative to its own largest entries (bf16 tokens in order: entries below 2^-20 of their column's
- * largest among 64 tokens are off by up to 2^-21 of it); a value that is not finite makes its column of S'
+ * largest among 64 tokens are off by up to 2^-21 of it, and the sums of 1024 tokens are truncated as they
+ * grow: values of one sign come out up to 2e-5 low); a value that is not finite makes its column of S'
  * so, and no other. The same inputs give the same bits. Errors as favor_decode_tree (L or
  * n_index above 2^30: FAVOR_ERR_UNSUPPORTED), and FAVOR_ERR_WORKSPACE.
  */

@@ -1122,9 +1122,14 @@ bool decode_supported(const favor_shape *s) {
 }
 
 // Whether a tree goes to the tensor cores' tiles (bf16). Up to 4 nodes the few-node kernel is faster at
-// any batch (d = 64, m = 256: 54 us for 1024 heads of 4 nodes, 8 for 8 heads; the tiles about 70 and 17
-// at any size up to 20 nodes), up to 16 the row kernel while its CTAs fit the SMs once (8 heads: 13 us at
-// 8 nodes, 16 at 16; but 90 and 108 for 1024 heads).
+// any batch, up to 16 the row kernel while its CTAs fit the SMs once. Times in us, few / rows / tiles:
+//                          d = 64, m = 256     d = 128, m = 256    d = 64, m = 32     d = 128, m = 32
+//    4 nodes,    8 heads   8.5 / 12.3 / 15.9   9.7 / 12.6 / 19.7   11.6 / 7.2 / 9.0   12.4 / 7.5 / 11.6
+//    4 nodes, 1024 heads    53 / 81 / 69       132 / 171 / 136      13 / 45 / 37       26 / 89 / 77
+//    8 nodes,    8 heads          13.5 / 15.7         13.9 / 19.8         8.2 / 9.0          8.5 / 11.7
+//   16 nodes,   64 heads          16.2 / 16.3         16.8 / 23.9        10.5 / 9.4         11.0 / 12.1
+//    8 nodes, 1024 heads            90 / 69            190 / 137           52 / 37           102 / 77
+//   32 nodes,   64 heads          19.4 / 16.5         37.7 / 20.7        13.4 / 9.7         24.5 / 12.3
 bool tree_on_tiles(const favor_shape *s) {
     if (s->dtype != FAVOR_BF16 || s->L <= 4) return false;
     return s->L > kRowsTile || (long long)s->B * s->H * (s->d / kRowsCols) > num_sms();
@@ -1133,8 +1138,13 @@ bool tree_on_tiles(const favor_shape *s) {
 // How favor_decode_extend takes n_tok tokens a head: on tiles (bf16 in order) or warp MMAs,
 // and the runs each head is cut into.
 //   Warp MMAs: up to kExtPath tokens (an accepted path) one CTA a head updates the state in place; more
-//   are cut so that the CTAs fill the SMs once (two to an SM up to 128 features).
-//   Tensor cores: as many runs of whole tiles as fill two CTAs an SM once (d = 128: kExtFlush tiles at most).
+//   are cut so that the CTAs fill the SMs once (two to an SM up to 128 features). For 1024 heads, in place /
+//   in runs: 16 tokens 35 / 60 us at d = 64, m = 256, 80 / 383 at d = 128 (4 tokens: 24 / 59, 64 / 379); at m =
+//   32 17 / 9 and 30 / 47. For 8 heads of 16 tokens 10.9 / 9.0 and 18.9 / 13.5.
+//   Tensor cores: as many runs of whole tiles as fill two CTAs an SM once (d = 128: kExtFlush tiles at most),
+//   from kExtTcMin tokens, one full tile, on. Warp MMAs / tiles at 64 tokens: d = 64, m = 256 13.8 / 7.2 us for 8
+//   heads, 100 / 71 for 1024, d = 128 15.4 / 15.6 and 472 / 361, m = 32 17 / 31 and 68 / 75 for 1024; at 32 tokens
+//   10.9 / 7.6, 73 / 70, 15.6 / 16.4, 413 / 365, 12 / 32, 54 / 77.
 constexpr int kExtTcMin = 64;
 constexpr int kExtMaxTokens = 1 << 30;  // (a run's end, one run past the last token, stays an int)
 struct ExtendPlan {
