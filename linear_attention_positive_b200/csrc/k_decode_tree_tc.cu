@@ -25,7 +25,7 @@
 // context, at most 0.02 % are behind 16 tokens and 0.05 to 0.6 % behind one.)
 //
 // T <= 64: keys and queries are the two halves of one 128-row tile, and at d = 64 two CTAs share an
-// SM (TMEM 256 columns, 111 KB), so that one head's copies and MMAs run under another's exponentials.
+// SM (TMEM 256 columns, 112 KB), so that one head's copies and MMAs run under another's exponentials.
 // T <= 128: a tile each, one CTA an SM.
 //
 // Features are taken 128 at a time (the logits of both halves are formed once for the maxima, then
