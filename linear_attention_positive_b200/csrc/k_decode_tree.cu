@@ -158,10 +158,13 @@ __device__ __noinline__ void tree_row_exact(const TreeParams &p, int bh, int i, 
 // The same for bf16 by warp MMAs (exact products), q and 7 visible nodes at a time, 64 features after
 // another with a running F, so that W is read once for 7 nodes and little is held: a lane has features
 // 16 f + 8 h + g of rows 2 t and 2 t + 1 (row 0: q), g = lane / 4, t = lane % 4. At m = 256 a row of some 25
-// nodes adds 40 us to a call at d = 64 and 80 at d = 128 (one node at a time, each lane reading its features'
-// rows of W, twice: 170 and 560).
+// nodes adds 40 us to a call at d = 64 and 75 at d = 128, 20 and 35 where four warps share it (one node at a
+// time, each lane reading its features' rows of W, twice: 170 and 560).
+// `parts` warps may share a row: groups of nodes and of features in turn; each then leaves its num, den and F
+// in part_out [D + 2] for tree_row_join.
 template <int D>
-__device__ __noinline__ void tree_row_exact_bf16(const TreeParams &p, int bh, int i, const int *par) {
+__device__ __noinline__ void tree_row_exact_bf16(const TreeParams &p, int bh, int i, const int *par, int part = 0,
+                                                 int parts = 1, float *part_out = nullptr) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, m = p.m;
     const size_t row0 = (size_t)bh * p.T * D;
     const float *S = p.state + (size_t)bh * ((size_t)D * m + 2 * m), *z = S + (size_t)D * m, *Dl = z + m;
@@ -173,13 +176,17 @@ __device__ __noinline__ void tree_row_exact_bf16(const TreeParams &p, int bh, in
     float num[D / 32], den = 0.f, dz = 0.f, F = -INFINITY;  // dz: the state's part of the denominator, this lane's features
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) num[k] = 0.f;
-    for (int j = i; j >= 0;) {
-        const bool first = j == i;  // the state is taken along
+    bool first = true;  // the state is taken along
+    for (int j = i, group = 0; j >= 0 || first; ++group) {
         int mine = -1;
 #pragma unroll
         for (int k = 1; k < 8; ++k) {
             if (k == g) mine = j;
             j = j >= 0 ? par[j] : -1;
+        }
+        if (group % parts != part) {
+            if (j >= 0 || !first) continue;
+            mine = -1;  // no nodes for this part, but its features of the state
         }
         const uint16_t *x = (const uint16_t *)(g == 0 ? p.q : p.k) + row0 + (size_t)(g == 0 ? i : max(mine, 0)) * D + 8 * t;
         uint4 xb[D / 32];
@@ -205,6 +212,7 @@ __device__ __noinline__ void tree_row_exact_bf16(const TreeParams &p, int bh, in
         }
 #pragma unroll 1
         for (int f0 = 0; f0 < m; f0 += 64) {
+            const bool state = first && (f0 >> 6) % parts == part;
             float u[4][4], e[8], top = -INFINITY;
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
@@ -224,7 +232,7 @@ __device__ __noinline__ void tree_row_exact_bf16(const TreeParams &p, int bh, in
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const float uq = __shfl_sync(0xffffffffu, u[f][2 * q], lane & 28);
-                    e[2 * f + q] = first && in && z[r + 8 * q] != 0.f ? uq + Dl[r + 8 * q] : -INFINITY;
+                    e[2 * f + q] = state && in && z[r + 8 * q] != 0.f ? uq + Dl[r + 8 * q] : -INFINITY;
                     u[f][2 * q] = in && use[0] ? uq + u[f][2 * q] - h[0] : -INFINITY;
                     u[f][2 * q + 1] = in && use[1] ? uq + u[f][2 * q + 1] - h[1] : -INFINITY;
                     top = fmax3(top, e[2 * f + q], fmaxf(u[f][2 * q], u[f][2 * q + 1]));
@@ -245,7 +253,7 @@ __device__ __noinline__ void tree_row_exact_bf16(const TreeParams &p, int bh, in
             for (int f = 0; f < 4; ++f)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) w[q & 1] += use[q & 1] && f0 + 16 * f < m ? expf(u[f][q] - F) : 0.f;
-            if (first) {
+            if (state) {
 #pragma unroll
                 for (int f = 0; f < 8; ++f) {
                     e[f] = e[f] == -INFINITY ? 0.f : expf(e[f] - F);
@@ -281,10 +289,37 @@ __device__ __noinline__ void tree_row_exact_bf16(const TreeParams &p, int bh, in
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) num[c] = y == 0.f ? num[c] : fmaf(y, v[k - 1][c], num[c]);
         }
+        first = false;
     }
     den += over_g(dz);
+    if (parts > 1) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) part_out[lane + 32 * c] = num[c];
+        if (lane == 0) part_out[D] = den;
+        if (lane == 0) part_out[D + 1] = F;
+        return;
+    }
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) p.out[row0 + (size_t)i * D + lane + 32 * c] = num[c] / den;
+}
+
+// Row i from its parts (one warp).
+template <int D>
+__device__ __forceinline__ void tree_row_join(const TreeParams &p, int bh, int i, int parts, const float *part_out) {
+    const int lane = threadIdx.x & 31;
+    float F = -INFINITY, num[D / 32], den = 0.f;
+    for (int k = 0; k < parts; ++k) F = fmaxf(F, part_out[k * (D + 2) + D + 1]);
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) num[c] = 0.f;
+    for (int k = 0; k < parts; ++k) {
+        const float *x = part_out + k * (D + 2);
+        const float w = x[D + 1] == -INFINITY ? 1.f : expf(x[D + 1] - F);  // (nothing in it, or no number)
+        den = fmaf(w, x[D], den);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) num[c] = fmaf(w, x[lane + 32 * c], num[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) p.out[((size_t)bh * p.T + i) * D + lane + 32 * c] = num[c] / den;
 }
 
 // sU[f][t0 + g] = w_(f0 + f) . x_g for 16 MT of a warp's features and 8 tokens (x: this lane's token row

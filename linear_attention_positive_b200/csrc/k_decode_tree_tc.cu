@@ -647,10 +647,31 @@ k_decode_tree_tc(const __grid_constant__ CUtensorMap mapQ, const __grid_constant
             const int r = i / (D / 4), c = i % (D / 4);
             if (sPtr[r]) *(float4 *)(out + (size_t)i * 4) = *(const float4 *)(sOut + r * D + ((c ^ (r & 7)) << 2));
         }
-        for (int r0 = 0, k = 0; r0 < n; r0 += 32) {  // the others, a warp a row in turn
-            uint32_t left = __ballot_sync(0xffffffffu, r0 + lane < n && !sPtr[r0 + lane]);
-            for (; left != 0; left &= left - 1)
-                if (k++ % (C::THREADS / 32) == warp) tree_row_exact_bf16<D>(p, bh, r0 + __ffs(left) - 1, sPar);
+        // the others: a warp a row in turn, or where there are few rows two or four warps
+        constexpr int NW = C::THREADS / 32;
+        uint32_t left[MR / 32];
+        int rows = 0;
+#pragma unroll
+        for (int w = 0; w < MR / 32; ++w) {
+            left[w] = __ballot_sync(0xffffffffu, 32 * w + lane < n && !sPtr[32 * w + lane]);
+            rows += __popc(left[w]);
+        }
+        if (rows != 0) {
+            const int parts = 4 * rows <= NW ? 4 : 2 * rows <= NW ? 2 : 1, share = NW / parts;
+            float *part_out = (float *)sXH;  // [row][part][D + 2]
+            int k = 0;
+            for (int w = 0; w < MR / 32; ++w)
+                for (uint32_t x = left[w]; x != 0; x &= x - 1, ++k)
+                    if (k % share == warp / parts)
+                        tree_row_exact_bf16<D>(p, bh, 32 * w + __ffs(x) - 1, sPar, warp % parts, parts,
+                                               part_out + (k * parts + warp % parts) * (D + 2));
+            if (parts > 1) {
+                __syncthreads();
+                k = 0;
+                for (int w = 0; w < MR / 32; ++w)
+                    for (uint32_t x = left[w]; x != 0; x &= x - 1, ++k)
+                        if (k == warp) tree_row_join<D>(p, bh, 32 * w + __ffs(x) - 1, parts, part_out + k * parts * (D + 2));
+            }
         }
     } while (false);
 
