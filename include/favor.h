@@ -263,9 +263,9 @@ FAVOR_API favor_status favor_decode_step(const favor_shape *shape, const void *q
  *   out          : device, fp32 [B,H,T,d]; rows from n_nodes[b] on are left as they were
  *   stream       : cudaStream_t as void*
  * q, k, v, W, state, out 16-byte aligned, parents and n_nodes 4-byte. The result has fp32 precision for
- * either dtype, in each value column relative to its own largest entries. What nodes outside J(i) hold never reaches row i, NaN and infinities included. Returns
- * FAVOR_ERR_INVALID_ARG, FAVOR_ERR_UNSUPPORTED (T above the limit, d not 64/128, m not a multiple of
- * 32 up to 256, B*H above 65535), FAVOR_ERR_CUDA.
+ * either dtype, in each value column relative to its own largest entries. What nodes outside J(i) hold
+ * never reaches row i, NaN and infinities included. Returns FAVOR_ERR_INVALID_ARG, FAVOR_ERR_UNSUPPORTED
+ * (T above the limit, d not 64/128, m not a multiple of 32 up to 256, B*H above 65535), FAVOR_ERR_CUDA.
  */
 FAVOR_API favor_status favor_decode_tree(const favor_shape *shape, const void *q, const void *k, const void *v,
                                          const void *W, const float *state, const int *parents, const int *n_nodes,
